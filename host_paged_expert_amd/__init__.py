@@ -2,8 +2,9 @@
 
 The work is done by libpe.so (C ABI in include/pe.h, HIP kernels in csrc/).
 This package is its thin ctypes binding plus `PagedMoE`, a small convenience
-owner of one context.  PyTorch is used by callers only for device memory and
-streams.
+owner of one context, and the dense operators around a paged layer on torch
+tensors (dense.py: rmsnorm, route, linear, glu, ffn_backward).  PyTorch is used
+by callers only for device memory and streams.
 """
 from ._binding import (  # noqa: F401
     LIB_PATH, PEError, lib,
@@ -17,7 +18,18 @@ from ._binding import (  # noqa: F401
     pe_suggest_k, pe_max_captured_batch, pe_max_waves, pe_get_lru_state, pe_get_plan, pe_get_slot_map, pe_get_stats,
     pe_reset_stats, pe_link_probe, pe_plan_host, pe_strerror, pe_last_error,
     pe_set_timing, pe_get_timing, STAGES,
+    PE_ACT_NONE, PE_ACT_SILU, PE_ACT_GELU, ACTS, PE_Y_BF16, PE_Y_FP32, PE_SCORE_SOFTMAX, PE_SCORE_SIGMOID, SCORES,
+    PE_MAX_NORM_HIDDEN,
+    pe_rmsnorm, pe_route, pe_linear, pe_glu, pe_ffn_backward,
 )
+
+
+def __getattr__(name):
+    # The tensor functions of dense.py import torch, which the rest of the package does without.
+    if name in ("rmsnorm", "route", "linear", "glu", "ffn_backward"):
+        from . import dense
+        return getattr(dense, name)
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
 
 
 class PagedMoE:

@@ -35,6 +35,17 @@ PE_FLAG_UNPAGED = 4
 PE_FLAG_PLAN_LOG = 8
 PE_STATIC_SCRATCH_BYTES = 16 << 20
 
+PE_ACT_NONE = 0
+PE_ACT_SILU = 1
+PE_ACT_GELU = 2
+ACTS = {"none": PE_ACT_NONE, "silu": PE_ACT_SILU, "gelu": PE_ACT_GELU}
+PE_Y_BF16 = 0
+PE_Y_FP32 = 1
+PE_SCORE_SOFTMAX = 0
+PE_SCORE_SIGMOID = 1
+SCORES = {"softmax": PE_SCORE_SOFTMAX, "sigmoid": PE_SCORE_SIGMOID}
+PE_MAX_NORM_HIDDEN = 16384
+
 
 class pe_config(ctypes.Structure):
     _fields_ = [("num_layers", ctypes.c_int), ("num_experts", ctypes.c_int), ("top_k", ctypes.c_int),
@@ -59,6 +70,7 @@ class PEError(RuntimeError):
 
 # Every symbol include/pe.h declares, with its ctypes signature.
 _vp, _i, _u32p, _i32p, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t
+_i64, _f = ctypes.c_int64, ctypes.c_float
 SIGNATURES = {
     "pe_create": (_i, [ctypes.POINTER(pe_config), ctypes.POINTER(ctypes.c_void_p)]),
     "pe_destroy": (None, [_vp]),
@@ -81,6 +93,12 @@ SIGNATURES = {
     "pe_plan_host": (_i, [_i, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
     "pe_set_timing": (_i, [_vp, _i]),
     "pe_get_timing": (_i, [_vp, _vp, _vp]),
+    "pe_rmsnorm": (_i, [_i, _vp, _i64, _vp, _i64, _vp, _f, _i, _i, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "pe_route": (_i, [_i, _vp, _i64, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp]),
+    "pe_linear": (_i, [_i, _i, _vp, _i64, _vp, _vp, _vp, _vp, _i, _vp, _i64, _i, _i, _i, _vp, _i64, _i, _vp]),
+    "pe_glu": (_i, [_i, _i, _i, _vp, _i64, _vp, _vp, _vp, _i, _i, _i, _vp, _i64, _vp, _vp, _vp]),
+    "pe_ffn_backward": (_i, [_i, _i, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _i64, _vp, _vp,
+                             _vp]),
     "pe_strerror": (ctypes.c_char_p, [_i]),
     "pe_last_error": (ctypes.c_char_p, []),
 }
@@ -314,6 +332,36 @@ def pe_get_timing(ctx):
     ms = np.zeros(len(STAGES), np.float64)
     _check(lib().pe_get_timing(ctx, n.ctypes.data, ms.ctypes.data))
     return {s: (int(n[i]), float(ms[i])) for i, s in enumerate(STAGES)}
+
+
+# The dense operators, with the C functions' arguments in their order.
+
+def pe_rmsnorm(device, x, ldx, residual, ldr, weight, eps, T, H, sum_out, lds, y, ldy, yscale=None, stream=None):
+    return _check(lib().pe_rmsnorm(device, _ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), eps, T, H, _ptr(sum_out),
+                                   lds, _ptr(y), ldy, _ptr(yscale), _stream(stream)))
+
+
+def pe_route(device, logits, ldl, T, num_experts, top_k, scoring, renormalize, scale, topk_ids, topk_w, stream=None):
+    return _check(lib().pe_route(device, _ptr(logits), ldl, T, num_experts, top_k, scoring, int(renormalize), scale,
+                                 _ptr(topk_ids), _ptr(topk_w), _stream(stream)))
+
+
+def pe_linear(device, wtype, x, ldx, xscale, w, wscale, bias, act, residual, ldr, T, N, K, y, ldy, ytype,
+              stream=None):
+    return _check(lib().pe_linear(device, wtype, _ptr(x), ldx, _ptr(xscale), _ptr(w), _ptr(wscale), _ptr(bias), act,
+                                  _ptr(residual), ldr, T, N, K, _ptr(y), ldy, ytype, _stream(stream)))
+
+
+def pe_glu(device, wtype, act, x, ldx, xscale, w13, s13, T, hidden, inter, h, ldh, hscale=None, gu=None, stream=None):
+    return _check(lib().pe_glu(device, wtype, act, _ptr(x), ldx, _ptr(xscale), _ptr(w13), _ptr(s13), T, hidden, inter,
+                               _ptr(h), ldh, _ptr(hscale), _ptr(gu), _stream(stream)))
+
+
+def pe_ffn_backward(device, act, dy, lddy, x, ldx, gu, w13, w2, T, hidden, inter, dgu, h, dx, lddx, dw13, dw2,
+                    stream=None):
+    return _check(lib().pe_ffn_backward(device, act, _ptr(dy), lddy, _ptr(x), ldx, _ptr(gu), _ptr(w13), _ptr(w2), T,
+                                        hidden, inter, _ptr(dgu), _ptr(h), _ptr(dx), lddx, _ptr(dw13), _ptr(dw2),
+                                        _stream(stream)))
 
 
 def pe_strerror(code):

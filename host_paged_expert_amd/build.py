@@ -7,7 +7,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libpe.so")
-SOURCES = ["csrc/pe_api.cpp", "csrc/pe_plan_host.cpp", "csrc/pe_kernels.hip"]
+SOURCES = ["csrc/pe_api.cpp", "csrc/pe_plan_host.cpp", "csrc/pe_dense_api.cpp", "csrc/pe_kernels.hip",
+           "csrc/pe_dense.hip"]
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
     "-ffp-contract=off",

@@ -17,14 +17,15 @@
 #include <vector>
 
 #include "../../include/pe.h"
+#include "pe_error.h"
 #include "pe_kernels.h"
 #include "pe_layout.h"
 
 namespace {
-
 thread_local std::string g_err;
+}  // namespace
 
-int fail(int code, const char* fmt, ...) {
+int pe::fail(int code, const char* fmt, ...) {
   char buf[512];
   va_list ap;
   va_start(ap, fmt);
@@ -34,13 +35,9 @@ int fail(int code, const char* fmt, ...) {
   return code;
 }
 
-#define PE_HIP(call)                                                                  \
-  do {                                                                                \
-    hipError_t e_ = (call);                                                           \
-    if (e_ != hipSuccess)                                                             \
-      return fail(PE_ERR_HIP, "%s failed: %s (line %d)", #call, hipGetErrorString(e_), \
-                  __LINE__);                                                          \
-  } while (0)
+using pe::fail;
+
+namespace {
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 

@@ -294,6 +294,105 @@ int pe_get_timing(pe_ctx* ctx, uint64_t* launches, double* total_ms);
 int pe_forward_static(pe_ctx* ctx, int layer, const void* x, const int32_t* topk_ids,
                       const float* topk_w, int T, void* out, void* stream);
 
+/* ---- dense operators around a paged layer ---------------------------------
+ *
+ * The parts of an MoE block beside its routed experts, in the order a block
+ * runs them: residual addition and RMS norm, router logits, top-k routing
+ * (whose ids and weights pe_forward takes), the gate/up half of the always-on
+ * shared expert or dense layer (W13 laid out as pe_load_expert takes it), its
+ * down projection, and that feed-forward block's gradients.
+ *
+ * They need no context, keep nothing between calls and allocate nothing: every
+ * call enqueues its launches on `stream` of `device` (the caller's current
+ * device is restored), may be captured into a hipGraph, and may run at the
+ * same time as any other call that does not write its buffers.  Matrices are
+ * row-major; a row stride (ld*) counts elements, is at least the row's length
+ * and below 2^31.  Matrices without one are contiguous.  Where nothing else is
+ * said, addresses and row strides are multiples of 16 bytes, outputs overlap
+ * no input and no other output, and T = 0 is a no-op.  Rows are independent
+ * of each other.  Sums are fp32. */
+
+/* activations */
+#define PE_ACT_NONE 0
+#define PE_ACT_SILU 1   /* v / (1 + exp(-v))               */
+#define PE_ACT_GELU 2   /* v * (1 + erf(v / sqrt(2))) / 2  */
+
+/* output types of pe_linear */
+#define PE_Y_BF16 0
+#define PE_Y_FP32 1
+
+/* router scores */
+#define PE_SCORE_SOFTMAX 0
+#define PE_SCORE_SIGMOID 1
+
+#define PE_MAX_NORM_HIDDEN 16384
+
+/* e4m3 activations: one fp32 scale per row and 128 columns, [T, C/128], value
+ * = code * scale.  The operators that make them take the group's largest
+ * magnitude m: scale = max(m / 448, 2^-126), code = the e4m3 number nearest
+ * value / scale.  A group with an infinity gets an infinite scale, and reads
+ * back as NaN. */
+
+/* Residual addition and root-mean-square norm of T rows:
+ *   v = x + residual (x alone if residual is NULL), in fp32;
+ *   sum = v rounded to bf16 (skipped if NULL);
+ *   y = v / sqrt(mean(v^2) + eps) * weight, from the unrounded v, as bf16, or
+ *       with yscale as e4m3 codes and scales (H a multiple of 128 then, of 8
+ *       otherwise; at most PE_MAX_NORM_HIDDEN).
+ * x, residual, sum bf16 [T, H], weight bf16 [H].  sum and a bf16 y may be x or
+ * residual itself.  e4m3 rows need 8-byte alignment only. */
+int pe_rmsnorm(int device, const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
+               float eps, int T, int H, void* sum, int64_t lds, void* y, int64_t ldy, float* yscale, void* stream);
+
+/* Top-k routing of T tokens: the top_k largest of each row's num_experts
+ * logits (fp32 [T, num_experts]; 4-byte alignment), in descending order, equal
+ * ones by ascending id: topk_ids int32 [T, top_k], topk_w fp32 [T, top_k] =
+ * scale * score, the score being the softmax over all of the row's logits or
+ * the sigmoid.  With `renormalize` the chosen scores are divided by their sum
+ * first (left as they are if it is 0).  Logits that are -infinity or NaN are never
+ * chosen and weigh nothing; where a row has fewer than top_k others, its last
+ * entries get id -1 and weight 0, which pe_forward skips (and counts in
+ * bad_ids).  num_experts <= 1024. */
+int pe_route(int device, const float* logits, int64_t ldl, int T, int num_experts, int top_k, int scoring,
+             int renormalize, float scale, int32_t* topk_ids, float* topk_w, void* stream);
+
+/* y[t,n] = act(sum_k x[t,k] w[n,k] + bias[n]) + residual[t,n], rounded once.
+ *   PE_W_BF16:     x bf16 [T, K], w bf16 [N, K], K a multiple of 8; scales NULL.
+ *   PE_W_FP8_B128: x e4m3 [T, K] with xscale [T, K/128], w e4m3 [N, K] with
+ *                  wscale [ceil(N/128), K/128], K a multiple of 128.
+ *   bias bf16 [N] or NULL, residual bf16 [T, N] or NULL, y bf16 or fp32 [T, N]
+ *   (ytype), of any alignment their elements have.  N is any number.
+ * A bf16 y may be the residual itself. */
+int pe_linear(int device, int wtype, const void* x, int64_t ldx, const float* xscale, const void* w,
+              const float* wscale, const void* bias, int act, const void* residual, int64_t ldr, int T, int N,
+              int K, void* y, int64_t ldy, int ytype, void* stream);
+
+/* The gate/up half of a gated feed-forward block: with w13 [2*inter, hidden],
+ * gate rows first, g = x W1^T and u = x W3^T, h[t,i] = act(g[t,i]) * u[t,i]
+ * (PE_ACT_SILU or PE_ACT_GELU).
+ *   x and w13 as in pe_linear (s13 fp32 [2*inter/128, hidden/128]); inter a
+ *   multiple of 8, of 128 for FP8 weights or with hscale.
+ *   h bf16 [T, inter], or with hscale e4m3 codes and scales, of any alignment
+ *   its elements have.
+ *   gu bf16 [T, 2*inter] or NULL: g and u, kept for pe_ffn_backward. */
+int pe_glu(int device, int wtype, int act, const void* x, int64_t ldx, const float* xscale, const void* w13,
+           const float* s13, int T, int hidden, int inter, void* h, int64_t ldh, float* hscale, void* gu,
+           void* stream);
+
+/* Gradients of y = h W2^T (h of pe_glu, bf16 weights, gu kept) for a given dy
+ * bf16 [T, hidden]:
+ *   dh = dy W2;  dg = dh * u * act'(g);  du = dh * act(g);
+ *   dx = dg W1 + du W3 [T, hidden];  dw13 = [dg, du]^T x [2*inter, hidden];
+ *   dw2 = dy^T h [hidden, inter]; all bf16, each skipped if NULL (not all).
+ * dgu bf16 [T, 2*inter] receives dg and du, and h bf16 [T, inter] (with dw2
+ * only; NULL otherwise) is made again from gu; both are read back by the
+ * products after them, as bf16.  w2 bf16 [hidden, inter].  hidden and inter
+ * are multiples of 8.  x may be NULL without dw13, w13 without dx.  A residual
+ * added to y has the gradient dy.  T = 0 sets dw13 and dw2 to zero. */
+int pe_ffn_backward(int device, int act, const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* gu,
+                    const void* w13, const void* w2, int T, int hidden, int inter, void* dgu, void* h, void* dx,
+                    int64_t lddx, void* dw13, void* dw2, void* stream);
+
 const char* pe_strerror(int status);
 const char* pe_last_error(void);
 

@@ -61,7 +61,7 @@ struct DenseArgs {
   float* hs;                  // GLU: [T, N / 128] scales of an e4m3 h, or nullptr
   uint16_t* gu;               // GLU: bf16 [T, 2N] to keep, or nullptr; DGLU: the kept one
   uint16_t* dgu;              // DGLU: bf16 [T, 2N]
-  int vec;                    // outputs, residual and bias may be accessed 4 columns at a time
+  int vec;                    // outputs, residual and bias may be accessed 8 columns at a time
 };
 
 void launch_rmsnorm(const NormArgs& a, hipStream_t s);

@@ -48,229 +48,935 @@ __device__ __forceinline__ float act_grad_f(float v, int act) {
   return 0.5f * (1.f + erff(v * 0.70710678f)) + v * __expf(-0.5f * v * v) * 0.39894228f;
 }
 
+// The value of another lane of the same 16: DPP controls of the butterfly below.
+template <int CTRL, class V>
+__device__ __forceinline__ V dpp(V v) {
+  return __builtin_bit_cast(
+      V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+
+// Combine the values of W consecutive lanes in all of them.  Up to 16 lanes by
+// DPP (pairs, pairs of pairs, mirrored halves of 8 and 16: after each stage every
+// lane of the smaller group already has the same value), wider by shuffles.
+template <int W, class V, class Op>
+__device__ __forceinline__ V group_reduce(V v, Op op) {
+  if constexpr (W >= 2) v = op(v, dpp<0xB1>(v));
+  if constexpr (W >= 4) v = op(v, dpp<0x4E>(v));
+  if constexpr (W >= 8) v = op(v, dpp<0x141>(v));
+  if constexpr (W >= 16) v = op(v, dpp<0x140>(v));
+  if constexpr (W >= 32) v = op(v, __shfl_xor(v, 16));
+  if constexpr (W >= 64) v = op(v, __shfl_xor(v, 32));
+  return v;
+}
 template <int W>
 __device__ __forceinline__ float group_max(float v) {
+  return group_reduce<W>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int W>
+__device__ __forceinline__ float group_sum(float v) {
+  return group_reduce<W>(v, [](float a, float b) { return a + b; });
+}
+
+// Four e4m3 codes of v / s, the first in the low byte.
+__device__ __forceinline__ uint32_t quant4(const float* v, float s) {
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] / s, v[1] / s, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2] / s, v[3] / s, lo, true);
+}
+
+// 8 bf16 values of a 16-byte chunk.
+__device__ __forceinline__ void widen8(const uint4& w, float (&v)[8]) {
+  const uint32_t d[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int m = W / 2; m; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
-  return v;
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(d[i] << 16);
+    v[2 * i + 1] = __uint_as_float(d[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ uint4 narrow8(const float (&v)[8]) {
+  uint32_t d[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] = f32_to_bf16(v[2 * i]) | (uint32_t)f32_to_bf16(v[2 * i + 1]) << 16;
+  return make_uint4(d[0], d[1], d[2], d[3]);
 }
 
 }  // namespace
 
 // ------------------------------------------------------------------ RMS norm
-
-// One workgroup per row: v = x + residual, y = v * rsqrt(mean(v^2) + eps) * weight.
-__global__ __launch_bounds__(128) void rmsnorm_kernel(NormArgs a) {
-  __shared__ float part[2];
-  const int64_t t = blockIdx.x;
-  const uint16_t* x = a.x + t * a.ldx;
-  const uint16_t* r = a.residual ? a.residual + t * a.ldr : nullptr;
-  float ss = 0.f;
-  for (int i = threadIdx.x; i < a.H; i += 128) {
-    const float v = bf16_to_f32(x[i]) + (r ? bf16_to_f32(r[i]) : 0.f);
-    ss += v * v;
-  }
+//
+// v = x + residual, y = v * rsqrt(mean(v^2) + eps) * weight: one pass, the row
+// in registers between the sum of squares and the output.  WPR wavefronts share
+// a row, each lane holding CH chunks of 8 columns; a scale group of 128 columns
+// is 16 neighbouring lanes.  Bound by its bytes: x, residual, sum and y once
+// each.  Rows of up to 1024 columns take one wavefront (no barrier), longer ones
+// the whole workgroup, which leaves a lane at most 8 chunks and gives a decode
+// step's few rows four wavefronts each.
+template <int WPR, int CH>
+__global__ __launch_bounds__(256) void rmsnorm_kernel(NormArgs a) {
+  __shared__ float part[4];
+  constexpr int kLanes = WPR * 64;
+  const int64_t t = (int64_t)blockIdx.x * (4 / WPR) + threadIdx.x / kLanes;
+  const int l = threadIdx.x % kLanes;
+  const bool row = t < a.T;
+  const int n_ch = row ? a.H / 8 : 0;
+  const uint4* x = reinterpret_cast<const uint4*>(a.x + t * a.ldx);
+  const uint4* r = reinterpret_cast<const uint4*>(a.residual + t * a.ldr);
+  const uint4* w = reinterpret_cast<const uint4*>(a.weight);
+  uint4 xc[CH], rc[CH], wc[CH];
 #pragma unroll
-  for (int m = 32; m; m >>= 1) ss += __shfl_xor(ss, m);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = ss;
-  __syncthreads();
-  const float inv = 1.f / sqrtf((part[0] + part[1]) / (float)a.H + a.eps);
-  for (int i0 = 0; i0 < a.H; i0 += 128) {
-    const int i = i0 + threadIdx.x;
-    const bool in = i < a.H;
-    const float v = in ? bf16_to_f32(x[i]) + (r ? bf16_to_f32(r[i]) : 0.f) : 0.f;
-    const float y = in ? v * inv * bf16_to_f32(a.weight[i]) : 0.f;
-    if (a.sum && in) a.sum[t * a.lds + i] = f32_to_bf16(v);
+  for (int i = 0; i < CH; ++i) {
+    const int c = l + i * kLanes;
+    xc[i] = rc[i] = wc[i] = make_uint4(0, 0, 0, 0);
+    if (c < n_ch) {
+      xc[i] = x[c];
+      if (a.residual) rc[i] = r[c];
+      wc[i] = w[c];
+    }
+  }
+  float v[CH][8], ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    float rv[8];
+    widen8(xc[i], v[i]);
+    widen8(rc[i], rv);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (a.residual) v[i][e] += rv[e];
+      ss = __builtin_fmaf(v[i][e], v[i][e], ss);
+    }
+  }
+  ss = group_sum<64>(ss);
+  if constexpr (WPR == 4) {
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = ss;
+    __syncthreads();
+    ss = (part[0] + part[1]) + (part[2] + part[3]);
+  }
+  const float inv = 1.f / sqrtf(ss / (float)a.H + a.eps);
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = l + i * kLanes;
+    float wv[8], y[8];
+    widen8(wc[i], wv);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = v[i][e] * inv * wv[e];
+    if (a.sum && c < n_ch) reinterpret_cast<uint4*>(a.sum + t * a.lds)[c] = narrow8(v[i]);
     if (!a.yscale) {
-      if (in) static_cast<uint16_t*>(a.y)[t * a.ldy + i] = f32_to_bf16(y);
+      if (c < n_ch) reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + t * a.ldy)[c] = narrow8(y);
       continue;
     }
-    __syncthreads();
-    const float m = group_max<64>(fabsf(y));
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
-    __syncthreads();
-    const float s = group_scale(fmaxf(part[0], part[1]));
-    static_cast<uint8_t*>(a.y)[t * a.ldy + i] = f32_to_e4m3(y / s);
-    if (threadIdx.x == 0) a.yscale[t * (a.H / 128) + i0 / 128] = s;
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
+    const float s = group_scale(group_max<16>(m));      // H is a multiple of 128: groups are whole
+    if (c < n_ch) {
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + t * a.ldy + c * 8) = make_uint2(quant4(y, s), quant4(y + 4, s));
+      if (c % 16 == 0) a.yscale[t * (a.H / 128) + c / 16] = s;
+    }
   }
 }
 
 void launch_rmsnorm(const NormArgs& a, hipStream_t s) {
-  rmsnorm_kernel<<<dim3(a.T), 128, 0, s>>>(a);
+  const dim3 one((a.T + 3) / 4), four(a.T);
+  if (a.H <= 512) rmsnorm_kernel<1, 1><<<one, 256, 0, s>>>(a);
+  else if (a.H <= 1024) rmsnorm_kernel<1, 2><<<one, 256, 0, s>>>(a);
+  else if (a.H <= 2048) rmsnorm_kernel<4, 1><<<four, 256, 0, s>>>(a);
+  else if (a.H <= 4096) rmsnorm_kernel<4, 2><<<four, 256, 0, s>>>(a);
+  else if (a.H <= 8192) rmsnorm_kernel<4, 4><<<four, 256, 0, s>>>(a);
+  else rmsnorm_kernel<4, 8><<<four, 256, 0, s>>>(a);
 }
 
 // ------------------------------------------------------------------ routing
-
-// One wavefront per token, lane l holding experts l, l + 64, ...: k rounds of
-// the largest remaining logit (ties to the lowest index).  Logits that are
-// -infinity or NaN are never chosen and weigh nothing.
-constexpr int kRoutePer = 16;    // 1024 experts / 64 lanes
-
-__global__ __launch_bounds__(64) void route_kernel(RouteArgs a) {
-  const int64_t t = blockIdx.x;
-  const int lane = threadIdx.x;
+//
+// LPT lanes per token, lane l holding experts l, l + LPT, ... (PER of them): k
+// rounds of the largest remaining logit, ties to the lowest id, so the choice
+// compares logits as they are, never rounded scores.  Logits that are -infinity
+// or NaN are never chosen and weigh nothing.  The fewest lanes that hold a
+// token's experts, 8 each, keep the butterflies short (all DPP up to 128
+// experts) and put several tokens on a wavefront.
+template <int LPT, int PER>
+__global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
+  const int64_t t = (int64_t)blockIdx.x * (256 / LPT) + threadIdx.x / LPT;
+  const int l = threadIdx.x % LPT;
+  if (t >= a.T) return;                                  // whole groups of LPT lanes leave
   const float kNone = -__builtin_inff();
-  float v[kRoutePer];
+  float v[PER];
   float mx = kNone;
 #pragma unroll
-  for (int j = 0; j < kRoutePer; ++j) {
-    const int e = lane + 64 * j;
-    const float l = e < a.E ? a.logits[t * a.ldl + e] : kNone;
-    v[j] = l == l ? l : kNone;
+  for (int j = 0; j < PER; ++j) {
+    const int e = l + LPT * j;
+    const float x = e < a.E ? a.logits[t * a.ldl + e] : kNone;
+    v[j] = x == x ? x : kNone;
     mx = fmaxf(mx, v[j]);
   }
-  mx = group_max<64>(mx);
+  mx = group_max<LPT>(mx);
   // softmax numerator of a logit (1 at the maximum, also where that is +infinity), or its sigmoid
-  auto num = [&](float l) {
-    if (l == kNone) return 0.f;
-    if (a.sigmoid) return 1.f / (1.f + expf(-l));
-    return l == mx ? 1.f : expf(l - mx);
+  auto num = [&](float x) {
+    if (x == kNone) return 0.f;
+    if (a.sigmoid) return 1.f / (1.f + expf(-x));
+    return x == mx ? 1.f : expf(x - mx);
   };
-  float den = 0.f;
+  float den = 1.f;
   if (!a.sigmoid) {
+    den = 0.f;
 #pragma unroll
-    for (int j = 0; j < kRoutePer; ++j) den += num(v[j]);
-#pragma unroll
-    for (int m = 32; m; m >>= 1) den += __shfl_xor(den, m);
+    for (int j = 0; j < PER; ++j) den += num(v[j]);
+    den = group_sum<LPT>(den);
   }
-  float chosen = 0.f;
+  // Round r's choice is kept by lane r % LPT: in registers for r < LPT, beyond that in the output.
+  int my_id = -1;
+  float my_p = 0.f, chosen = 0.f;
   for (int r = 0; r < a.k; ++r) {
     float best = kNone;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) best = fmaxf(best, v[j]);
+    best = group_max<LPT>(best);
     int at = 1 << 30;
+    if (best > kNone) {
 #pragma unroll
-    for (int j = 0; j < kRoutePer; ++j)
-      if (v[j] > best) { best = v[j]; at = lane + 64 * j; }
-#pragma unroll
-    for (int m = 32; m; m >>= 1) {
-      const float ob = __shfl_xor(best, m);
-      const int oa = __shfl_xor(at, m);
-      if (ob > best || (ob == best && oa < at)) { best = ob; at = oa; }
+      for (int j = PER - 1; j >= 0; --j)
+        if (v[j] == best) at = l + LPT * j;
     }
-    const bool found = best > kNone;
-    const float p = !found ? 0.f : a.sigmoid ? num(best) : num(best) / den;
+    at = group_reduce<LPT>(at, [](int p, int q) { return min(p, q); });
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (at == l + LPT * j) v[j] = kNone;
+    const float p = best > kNone ? num(best) / den : 0.f;
     chosen += p;
-    if (lane == 0) {
-      a.ids[t * a.k + r] = found ? at : -1;
-      a.w[t * a.k + r] = p * a.scale;
+    if (l == r % LPT) {
+      const int id = best > kNone ? at : -1;
+      if (r < LPT) {
+        my_id = id;
+        my_p = p;
+      } else {
+        a.ids[t * a.k + r] = id;
+        a.w[t * a.k + r] = p;
+      }
     }
-#pragma unroll
-    for (int j = 0; j < kRoutePer; ++j)
-      if (at == lane + 64 * j) v[j] = kNone;
   }
-  if (a.renorm && chosen > 0.f && lane == 0)
-    for (int r = 0; r < a.k; ++r) a.w[t * a.k + r] = a.w[t * a.k + r] / chosen;
+  const float by = a.renorm && chosen > 0.f ? chosen : 1.f;
+  if (l < a.k) {
+    a.ids[t * a.k + l] = my_id;
+    a.w[t * a.k + l] = my_p / by * a.scale;
+  }
+  for (int r = l + LPT; r < a.k; r += LPT) a.w[t * a.k + r] = a.w[t * a.k + r] / by * a.scale;
+}
+
+template <int LPT, int PER>
+static void launch_route_n(const RouteArgs& a, hipStream_t s) {
+  const int per = 256 / LPT;
+  route_kernel<LPT, PER><<<dim3((a.T + per - 1) / per), 256, 0, s>>>(a);
 }
 
 void launch_route(const RouteArgs& a, hipStream_t s) {
-  route_kernel<<<dim3(a.T), 64, 0, s>>>(a);
+  if (a.E <= 64) launch_route_n<8, 8>(a, s);
+  else if (a.E <= 128) launch_route_n<16, 8>(a, s);
+  else if (a.E <= 256) launch_route_n<32, 8>(a, s);
+  else if (a.E <= 512) launch_route_n<64, 8>(a, s);
+  else launch_route_n<64, 16>(a, s);
 }
 
-// ------------------------------------------------------------------ matrix products
+// ------------------------------------------------------------------ matrix products, tiled
+//
+// out[t, n] = sum_k A[t, k] B[n, k] on the matrix cores, a BT x BN tile per
+// workgroup.  Both operands come through LDS in steps of 128 bytes of k (64
+// bf16, 128 e4m3 values: one scale group), NST stages deep: each wavefront
+// copies its share of a later step straight from global memory into LDS (no
+// registers), while the step that has arrived feeds the MFMAs.  One barrier per
+// step: it follows each wavefront's wait for its own copies, so the step is
+// whole, and every wavefront is then done reading the buffer the next copies
+// overwrite.
+//
+// A K-major operand's tile is [rows][128 bytes]; a k-slow operand (a gradient's
+// transposed factor) is [64 k][rows], and the transposing LDS read gives each
+// lane four consecutive k of its row.  LDS-direct copies write lane after lane,
+// so bank conflicts are avoided by permuting which global chunk a lane fetches:
+// K-major rows keep their 16-byte chunk c at position c ^ (row / 2 % 8) (the 16
+// rows one read touches fall on all 16 chunk slots of two rows), k-slow rows
+// their 32-byte unit u at u ^ f(k), with f different for the rows of one read.
+//
+// The MFMA takes B's rows as its first operand, so a lane's four accumulators
+// are four consecutive n of one t: 8-byte stores, vector loads of the residual.
+// FP8 operands with bf16 outputs take v_mfma_f32_16x16x128_f8f6f4; the step's
+// partial products are multiplied by the row's and the block's fp32 scale when
+// they are added up in fp32.  Inside, the instruction lines up the eight products
+// of eight consecutive k to the largest of their exponents and drops what lies
+// more than 13 bits below it (measured product by product); the sums of eight are
+// added in fp32.  Each product is so off by less than 2^-13 of the largest of its
+// eight: below the output's own rounding.  Where an output is kept in fp32 (y, or
+// the scales of an e4m3 h) the codes are widened to bf16 in registers instead, for
+// full-width sums at half the matrix rate.
+//
+// Rows past the end are read as the last row (their results are not stored); k
+// past the end is read from a page of zeros.
 
-// A 32 x 128 tile of the output per workgroup, fp32 arithmetic on operands
-// staged in LDS 16 values of k at a time; each thread has 4 x 4 outputs.
-template <DenseOp OP, bool FP8, bool AK, bool BK>
-__global__ __launch_bounds__(256) void dense_kernel(DenseArgs a) {
-  constexpr int MT = 32, MN = 128, KB = 16, NB = OP == DENSE_GLU ? 2 : 1;
-  __shared__ float sa[KB][MT + 1];
-  __shared__ float sb[NB][KB][MN + 1];
-  const int t0 = blockIdx.y * MT, n0 = blockIdx.x * MN;
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int64_t nk = a.K / 128;
-  auto left = [&](int t, int k) {
-    if (t >= a.T || k >= a.K) return 0.f;
-    if constexpr (FP8)
-      return e4m3_to_f32(static_cast<const uint8_t*>(a.a)[t * a.lda + k]) * a.as[t * nk + k / 128];
-    else
-      return bf16_to_f32(static_cast<const uint16_t*>(a.a)[AK ? t * a.lda + k : k * a.lda + t]);
-  };
-  auto right = [&](int n, int k, int part) {
-    if (n >= a.N || k >= a.K) return 0.f;
-    const int64_t row = (int64_t)part * a.N + n;
-    if constexpr (FP8)
-      return e4m3_to_f32(static_cast<const uint8_t*>(a.b)[row * a.ldb + k]) * a.bs[(row / 128) * nk + k / 128];
-    else
-      return bf16_to_f32(static_cast<const uint16_t*>(a.b)[BK ? row * a.ldb + k : k * a.ldb + n]);
-  };
-  float acc[NB][4][4] = {};
-  for (int k0 = 0; k0 < a.K; k0 += KB) {
-    for (int i = threadIdx.x; i < KB * MT; i += 256) {
-      const int k = AK ? i % KB : i / MT, t = AK ? i / KB : i % MT;
-      sa[k][t] = left(t0 + t, k0 + k);
+namespace {
+
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
+typedef __attribute__((ext_vector_type(4))) float f32x4_t;
+typedef __attribute__((ext_vector_type(4))) short s16x4_t;
+typedef __attribute__((ext_vector_type(8))) int i32x8_t;
+
+__device__ __attribute__((aligned(16))) const uint32_t g_zeros[4] = {0, 0, 0, 0};
+
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)(const char*)p;
+}
+
+// Copy 16 bytes per lane from base + off (64 lanes) to the 1024 bytes of LDS at
+// `lds` (wavefront-uniform).  The compiler orders LDS-direct loads against
+// every LDS read it sees with a full wait, which would end the pipelining; as
+// inline assembly without outputs they are ordered by wait_stage alone.
+__device__ __forceinline__ void copy_to_lds(uint32_t lds, const char* base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base));
+}
+__device__ __forceinline__ void copy_to_lds(uint32_t lds, const char* p) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p));
+}
+// Same for 4 bytes per lane to 256 bytes of LDS.
+__device__ __forceinline__ void copy_to_lds4(uint32_t lds, const char* p) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(p));
+}
+
+// This wavefront's copies are done but for the newest N, its LDS reads are
+// done, and so are every other wavefront's.
+template <int N>
+__device__ __forceinline__ void wait_stage() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// Eight e4m3 codes as bf16 (exactly).
+__device__ __forceinline__ bf16x8_t widen_e4m3(uint32_t lo, uint32_t hi) {
+  typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
+  const bf16x2_t p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+  const bf16x2_t p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+  const bf16x2_t p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+  const bf16x2_t p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+  return bf16x8_t{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+
+// One operand's tile of ROWS rows: what this wavefront copies per step, and
+// where its lanes read fragments.
+template <int ROWS, int NW, bool KMAJOR>
+struct Operand {
+  static constexpr int kInstr = ROWS / 8;               // 1024-byte copies per step
+  static constexpr int kPer = kInstr / NW;              // of which per wavefront
+  static_assert(kInstr % NW == 0 && NW % 2 == 0, "copies divide evenly");
+
+  uint32_t off[kPer];     // K-major: byte offset of the lane's chunk from the tile's first row; k-slow: from row k0
+  int kc[kPer];           // K-major: the chunk's byte within the 128; k-slow: its k row
+
+  // `row(r)`: the matrix row (clamped) of tile row r, relative to the tile's base; ld in bytes
+  template <class RowOf>
+  __device__ __forceinline__ void init(int wave, int lane, int64_t ld, RowOf row, int c0, int n_cols) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int j = wave + i * NW;
+      if constexpr (KMAJOR) {
+        const int r = 8 * j + (lane >> 3);
+        const int c = (lane & 7) ^ ((r >> 1) & 7);
+        kc[i] = c * 16;
+        off[i] = (uint32_t)(row(r) * ld) + c * 16;
+      } else {
+        constexpr int CPR = ROWS / 8;                   // 16-byte chunks per k row
+        const int idx = 64 * j + lane, k = idx / CPR, pos = idx % CPR;
+        const int c = (((pos >> 1) ^ swz(k)) << 1) | (pos & 1);
+        kc[i] = k;
+        // columns past the end are read as the last chunk of the row
+        off[i] = (uint32_t)(k * ld) + 2 * min(c0 + 8 * c, n_cols - 8);
+      }
     }
-    for (int p = 0; p < NB; ++p)
-      for (int i = threadIdx.x; i < KB * MN; i += 256) {
-        const int k = BK ? i % KB : i / MN, n = BK ? i / KB : i % MN;
-        sb[p][k][n] = right(n0 + n, k0 + k, p);
-      }
-    __syncthreads();
-    for (int k = 0; k < KB; ++k)
-#pragma unroll
-      for (int p = 0; p < NB; ++p)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            acc[p][i][j] = __builtin_fmaf(sa[k][ty * 4 + i], sb[p][k][tx * 4 + j], acc[p][i][j]);
-    __syncthreads();
   }
+
+  static __device__ __forceinline__ int swz(int k) {
+    if constexpr (ROWS >= 128) return (k & 3) | ((k >> 1) & 4);
+    return ((k >> 1) & 1) | ((k >> 2) & 2);
+  }
+
+  // Copy the step whose first chunk (or k row) is at `base`.
+  __device__ __forceinline__ void copy(uint32_t lds, int wave, const char* base) const {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t t = t0 + ty * 4 + i;
-    const bool in_t = t < a.T;
-    if constexpr (OP == DENSE_LINEAR) {
-      for (int j = 0; j < 4; ++j) {
-        const int n = n0 + tx * 4 + j;
-        if (!in_t || n >= a.N) continue;
-        float v = act_f(acc[0][i][j] + (a.bias ? bf16_to_f32(a.bias[n]) : 0.f), a.act);
-        if (a.residual) v += bf16_to_f32(a.residual[t * a.ldr + n]);
-        if (a.y_f32) static_cast<float*>(a.y)[t * a.ldy + n] = v;
-        else static_cast<uint16_t*>(a.y)[t * a.ldy + n] = f32_to_bf16(v);
-      }
-    } else if constexpr (OP == DENSE_GLU) {
-      float h[4], m = 0.f;
-      for (int j = 0; j < 4; ++j) {
-        const int n = n0 + tx * 4 + j;
-        const float g = acc[0][i][j], u = acc[NB - 1][i][j];
-        h[j] = act_f(g, a.act) * u;
-        m = fmaxf(m, fabsf(h[j]));
-        if (a.gu && in_t && n < a.N) {
-          a.gu[t * 2 * a.N + n] = f32_to_bf16(g);
-          a.gu[t * 2 * a.N + a.N + n] = f32_to_bf16(u);
+    for (int i = 0; i < kPer; ++i) copy_to_lds(lds + (wave + i * NW) * 1024, base, off[i]);
+  }
+  // The same where only the first `valid` bytes (k rows) of the step exist.
+  __device__ __forceinline__ void copy_tail(uint32_t lds, int wave, const char* base, int valid) const {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      copy_to_lds(lds + (wave + i * NW) * 1024,
+                  kc[i] < valid ? base + off[i] : reinterpret_cast<const char*>(g_zeros));
+  }
+};
+
+// Fragment reads of rows w0 .. w0 + 16 F - 1 of an operand's tile.
+template <int ROWS, bool KMAJOR, int F>
+struct Frags {
+  uint32_t at[KMAJOR ? 2 : F];
+
+  __device__ __forceinline__ void init(int w0, int lane) {
+    const int q = lane >> 4, j = lane & 15;
+    if constexpr (KMAJOR) {
+      const uint32_t row = (w0 + j) * 128;
+      at[0] = row + ((q ^ (j >> 1)) << 4);
+      at[1] = at[0] ^ 64;
+    } else {
+      const int k = 8 * q + (j >> 2);
+      const int g = Operand<ROWS, 2, false>::swz(k);
+#pragma unroll
+      for (int f = 0; f < F; ++f) at[f] = k * ROWS * 2 + (((w0 / 16 + f) ^ g) << 5) + (j & 3) * 8;
+    }
+  }
+
+  // Fragment f of k values 32 s .. 32 s + 31 of the step staged at `stage`.
+  __device__ __forceinline__ bf16x8_t bf16(const char* stage, int f, int s) const {
+    if constexpr (KMAJOR) {
+      return *reinterpret_cast<const bf16x8_t*>(stage + at[s] + f * 2048);
+    } else {
+      typedef __attribute__((address_space(3))) s16x4_t* tr_p;
+      const char* p = stage + at[f] + s * 32 * ROWS * 2;
+      const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_p)(uintptr_t)lds_addr(p));
+      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_p)(uintptr_t)lds_addr(p + 4 * ROWS * 2));
+      return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  }
+  // Fragment f of the whole step in e4m3: both operands take the two chunks in
+  // this order, so the pairing of k values is right whatever order the MFMA has.
+  __device__ __forceinline__ i32x8_t fp8(const char* stage, int f) const {
+    const uint4 lo = *reinterpret_cast<const uint4*>(stage + at[0] + f * 2048);
+    const uint4 hi = *reinterpret_cast<const uint4*>(stage + at[1] + f * 2048);
+    return i32x8_t{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+  }
+};
+
+// C (4 or 8) consecutive bf16 values: as one vector, or the first n of them.
+template <int C>
+__device__ __forceinline__ void load_bf16(const uint16_t* p, bool vec, int n, float (&v)[C]) {
+  if (vec) {
+    uint32_t w[C / 2];
+    if constexpr (C == 8) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+    else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = i < n ? bf16_to_f32(p[i]) : 0.f;
+  }
+}
+template <int C>
+__device__ __forceinline__ void store_bf16(uint16_t* p, bool vec, int n, const float (&v)[C]) {
+  if (vec) {
+    uint32_t w[C / 2];
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) w[i] = f32_to_bf16(v[2 * i]) | (uint32_t)f32_to_bf16(v[2 * i + 1]) << 16;
+    if constexpr (C == 8) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(w);
+    else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (i < n) p[i] = f32_to_bf16(v[i]);
+  }
+}
+
+// y[t, n .. n + C - 1] = act(v + bias) + residual.
+template <int C>
+__device__ __forceinline__ void finish_linear(const DenseArgs& a, int64_t t, int n, float (&v)[C]) {
+  const int left = a.N - n;
+  const bool vec = a.vec && left >= C;
+  float w[C];
+  if (a.bias) {
+    load_bf16(a.bias + n, vec, left, w);
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] += w[i];
+  }
+  if (a.act != PE_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = act_f(v[i], a.act);
+  }
+  if (a.residual) {
+    load_bf16(a.residual + t * a.ldr + n, vec, left, w);
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] += w[i];
+  }
+  if (!a.y_f32) {
+    store_bf16(static_cast<uint16_t*>(a.y) + t * a.ldy + n, vec, left, v);
+  } else {
+    float* y = static_cast<float*>(a.y) + t * a.ldy + n;
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < C; i += 4) *reinterpret_cast<float4*>(y + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        if (i < left) y[i] = v[i];
+    }
+  }
+}
+
+// h[t, n .. n + C - 1] = act(g) * u, and g and u themselves if they are kept.
+// With e4m3 output the 128 / C lanes of a scale group hold its columns in order
+// (all of them come here, `in` saying whether the row exists).
+template <int C>
+__device__ __forceinline__ void finish_glu(const DenseArgs& a, int64_t t, int n, bool in, const float (&g)[C],
+                                           const float (&u)[C]) {
+  float h[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) h[i] = act_f(g[i], a.act) * u[i];
+  if (a.gu && in) {                                     // 16-byte aligned rows, N a multiple of 8
+    store_bf16(a.gu + t * 2 * a.N + n, true, C, g);
+    store_bf16(a.gu + t * 2 * a.N + a.N + n, true, C, u);
+  }
+  if (!a.hs) {
+    if (in) store_bf16(static_cast<uint16_t*>(a.y) + t * a.ldy + n, a.vec, C, h);
+    return;
+  }
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < C; ++i) m = fmaxf(m, fabsf(h[i]));
+  const float s = group_scale(group_max<128 / C>(m));
+  if (!in) return;
+  if (n % 128 == 0) a.hs[t * (a.N / 128) + n / 128] = s;
+  uint8_t* y = static_cast<uint8_t*>(a.y) + t * a.ldy + n;
+#pragma unroll
+  for (int i = 0; i < C; i += 4) {
+    const uint32_t c = quant4(h + i, s);
+    if (a.vec) {
+      *reinterpret_cast<uint32_t*>(y + i) = c;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[i + e] = (uint8_t)(c >> (8 * e));
+    }
+  }
+}
+
+// From dh[t, n .. n + C - 1] and the kept g and u: their gradients, and h.
+template <int C>
+__device__ __forceinline__ void finish_dglu(const DenseArgs& a, int64_t t, int n, const float (&dh)[C]) {
+  float g[C], u[C], dg[C], du[C], h[C];
+  load_bf16(a.gu + t * 2 * a.N + n, true, C, g);
+  load_bf16(a.gu + t * 2 * a.N + a.N + n, true, C, u);
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const float ag = act_f(g[i], a.act);
+    dg[i] = dh[i] * u[i] * act_grad_f(g[i], a.act);
+    du[i] = dh[i] * ag;
+    h[i] = ag * u[i];
+  }
+  store_bf16(a.dgu + t * 2 * a.N + n, true, C, dg);
+  store_bf16(a.dgu + t * 2 * a.N + a.N + n, true, C, du);
+  if (a.y) store_bf16(static_cast<uint16_t*>(a.y) + t * a.ldy + n, true, C, h);
+}
+
+// Workgroups go round-robin over the 8 XCDs, each with its own L2.  Every XCD
+// takes a contiguous run of tiles, in bands of kBand tiles of t, column by
+// column, so that the tiles in flight together share rows of both operands.
+__device__ __forceinline__ void tile_of(int nt, int nn, int& tt, int& tn) {
+  constexpr int kXcds = 8, kBand = 8;
+  const int total = nt * nn, b = blockIdx.x;
+  const int xcd = b % kXcds, per = total / kXcds, rem = total % kXcds;
+  const int q = xcd * per + min(xcd, rem) + b / kXcds;
+  const int band = q / (kBand * nn), rows = min(kBand, nt - band * kBand), r = q - band * kBand * nn;
+  tt = band * kBand + r % rows;
+  tn = r / rows;
+}
+
+}  // namespace
+
+// LDS of a tile kernel: the stages of both operands and, after them, the fp32 tile.
+constexpr int tile_lds(int bt, int bn, int nst, int fp8) {
+  const int stages = nst * ((bt + bn) * 128 + (fp8 ? bt * 4 : 0)), tile = bt * (bn + 4) * 4;
+  return stages > tile ? stages : tile;
+}
+
+// FP8: 0 bf16 operands, 1 e4m3 through the FP8 MFMA, 2 e4m3 widened to bf16.
+// A WT x WN grid of wavefronts, each with FT x FN blocks of 16 x 16 outputs.
+// A GLU tile's B rows alternate 16 gate rows and the 16 up rows of the same
+// columns, so that a wavefront holds both products of its columns.
+template <DenseOp OP, int FP8, bool AK, bool BK, int WT, int WN, int FT, int FN, int NST>
+__global__ __launch_bounds__(WT * WN * 64) void dense_tile_kernel(DenseArgs a) {
+  constexpr int NW = WT * WN, BT = WT * FT * 16, BN = WN * FN * 16;
+  constexpr int NO = OP == DENSE_GLU ? BN / 2 : BN;       // output columns per tile
+  constexpr int ES = FP8 ? 1 : 2;
+  constexpr int kA = BT * 128, kB = BN * 128, kStage = kA + kB + (FP8 ? BT * 4 : 0);
+  extern __shared__ __align__(16) char lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wt = wave / WN, wn = wave % WN;
+  const int q4 = (lane >> 4) * 4, ln = lane & 15;
+  int tt, tn;
+  tile_of((a.T + BT - 1) / BT, (a.N + NO - 1) / NO, tt, tn);
+  const int t0 = tt * BT, n0 = tn * NO;
+  const int64_t lda = a.lda * ES, ldb = a.ldb * ES;
+
+  Operand<BT, NW, AK> oa;
+  Operand<BN, NW, BK> ob;
+  const char* pa = static_cast<const char*>(a.a) + (AK ? t0 * lda : 0);
+  const char* pb = static_cast<const char*>(a.b) + (BK ? n0 * ldb : 0);
+  oa.init(wave, lane, lda, [&](int r) { return (int64_t)min(r, a.T - 1 - t0); }, t0, a.T);
+  // the up half's rows can be further than 32-bit offsets reach: OP == GLU adds them to the base of its copies
+  ob.init(wave, lane, ldb, [&](int r) {
+    if constexpr (OP == DENSE_GLU) return (int64_t)min((r >> 5) * 16 + (r & 15), a.N - 1 - n0);
+    return (int64_t)min(r, a.N - 1 - n0);
+  }, n0, a.N);
+  Frags<BT, AK, FT> fa;
+  Frags<BN, BK, FN> fb;
+  fa.init(wt * FT * 16, lane);
+  fb.init(wn * FN * 16, lane);
+
+  const int64_t sa = AK ? 128 : 64 * lda, sb = BK ? 128 : 64 * ldb;    // bytes per step
+  constexpr int kstep = 128 / ES;
+  const int nk = (a.K + kstep - 1) / kstep;
+  const int tail = a.K - (nk - 1) * kstep;                              // k of the last step
+  const int64_t up = OP == DENSE_GLU ? (int64_t)a.N * ldb : 0;
+  const uint32_t lds0 = lds_addr(lds);
+  // this wavefront copies 8-row pieces wave, wave + NW, ...: with a GLU's 16-row alternation and NW a
+  // multiple of 4, they all lie in one half
+  static_assert(OP != DENSE_GLU || NW % 4 == 0, "a wavefront's copies stay in one half");
+  if (OP == DENSE_GLU && (wave & 2)) pb += up;
+  const int scales_k = FP8 ? a.K / 128 : 0;
+  const char* ps = nullptr;
+  if constexpr (FP8)
+    ps = reinterpret_cast<const char*>(a.as + (int64_t)min(t0 + (int)threadIdx.x, a.T - 1) * scales_k);
+
+  auto fetch = [&](int k) {      // copies of step k
+    const uint32_t st = lds0 + (k % NST) * kStage;
+    if (k < nk - 1 || tail == kstep) {
+      oa.copy(st, wave, pa + k * sa);
+      ob.copy(st + kA, wave, pb + k * sb);
+    } else {
+      oa.copy_tail(st, wave, pa + k * sa, AK ? tail * ES : tail);
+      ob.copy_tail(st + kA, wave, pb + k * sb, BK ? tail * ES : tail);
+    }
+    if constexpr (FP8)
+      if (wave < BT / 64) copy_to_lds4(st + kA + kB + wave * 256, ps + k * 4);
+  };
+  constexpr int kCopies = decltype(oa)::kPer + decltype(ob)::kPer;     // per step (wavefronts with scales: one more)
+
+  f32x4_t acc[FT][FN];
+#pragma unroll
+  for (int i = 0; i < FT; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  // FP8: the scale of this wavefront's weight rows (they lie in one 128-row block; a GLU's two halves in one each)
+  const int brow = n0 + (OP == DENSE_GLU ? wn * FN * 8 : wn * FN * 16);
+  const float* sw0 = nullptr;
+  const float* sw1 = nullptr;
+  if constexpr (FP8) {
+    static_assert(FN * 16 <= 128, "a wavefront's columns lie in one scale block");
+    sw0 = a.bs + (int64_t)(min(brow, a.N - 1) / 128) * scales_k;
+    sw1 = OP == DENSE_GLU ? a.bs + (int64_t)((a.N + min(brow, a.N - 1)) / 128) * scales_k : sw0;
+  }
+
+#pragma unroll
+  for (int k = 0; k < NST - 1; ++k)
+    if (k < nk) fetch(k);
+  for (int k = 0; k < nk; ++k) {
+    if (NST > 2 && k + NST - 2 < nk) wait_stage<(NST - 2) * kCopies>();
+    else wait_stage<0>();
+    const char* st = lds + (k % NST) * kStage;
+    if constexpr (FP8) {
+      if (k + NST - 1 < nk) fetch(k + NST - 1);
+      const float* sc = reinterpret_cast<const float*>(st + kA + kB) + wt * FT * 16 + ln;
+      const float w0 = sw0[k], w1 = sw1[k];
+      i32x8_t bf[FP8 == 1 ? FN : 1];
+      bf16x8_t bw[FP8 == 2 ? FN : 1][4];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        if constexpr (FP8 == 1) {
+          bf[j] = fb.fp8(st + kA, j);
+        } else {
+          const i32x8_t v = fb.fp8(st + kA, j);
+#pragma unroll
+          for (int s = 0; s < 4; ++s) bw[j][s] = widen_e4m3(v[2 * s], v[2 * s + 1]);
         }
       }
-      // the 32 threads of a row hold one group of 128 columns
-      const float s = group_scale(group_max<32>(m));
-      for (int j = 0; j < 4; ++j) {
-        const int n = n0 + tx * 4 + j;
-        if (!in_t || n >= a.N) continue;
-        if (a.hs) static_cast<uint8_t*>(a.y)[t * a.ldy + n] = f32_to_e4m3(h[j] / s);
-        else static_cast<uint16_t*>(a.y)[t * a.ldy + n] = f32_to_bf16(h[j]);
+#pragma unroll
+      for (int i = 0; i < FT; ++i) {
+        const i32x8_t af = fa.fp8(st, i);
+        const float s0 = sc[16 * i] * w0, s1 = sc[16 * i] * w1;
+        bf16x8_t aw[4];
+        if constexpr (FP8 == 2) {
+#pragma unroll
+          for (int s = 0; s < 4; ++s) aw[s] = widen_e4m3(af[2 * s], af[2 * s + 1]);
+        }
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          f32x4_t p = f32x4_t{0.f, 0.f, 0.f, 0.f};
+          if constexpr (FP8 == 2) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bw[j][s], aw[s], p, 0, 0, 0);
+          } else {
+            p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                bf[j], af, p, 0, 0, 0, 0, 0, 0);   // no block scales
+          }
+          const float s = OP == DENSE_GLU && (j & 1) ? s1 : s0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[e], s, acc[i][j][e]);
+        }
       }
-      if (a.hs && in_t && tx == 0) a.hs[t * (a.N / 128) + n0 / 128] = s;
     } else {
-      for (int j = 0; j < 4; ++j) {
-        const int n = n0 + tx * 4 + j;
-        if (!in_t || n >= a.N) continue;
-        const float g = bf16_to_f32(a.gu[t * 2 * a.N + n]), u = bf16_to_f32(a.gu[t * 2 * a.N + a.N + n]);
-        const float dh = acc[0][i][j], ag = act_f(g, a.act);
-        a.dgu[t * 2 * a.N + n] = f32_to_bf16(dh * u * act_grad_f(g, a.act));
-        a.dgu[t * 2 * a.N + a.N + n] = f32_to_bf16(dh * ag);
-        if (a.y) static_cast<uint16_t*>(a.y)[t * a.ldy + n] = f32_to_bf16(ag * u);
+      if (k + NST - 1 < nk) fetch(k + NST - 1);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        bf16x8_t af[FT], bf[FN];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) bf[j] = fb.bf16(st + kA, j, s);
+#pragma unroll
+        for (int i = 0; i < FT; ++i) af[i] = fa.bf16(st, i, s);
+#pragma unroll
+        for (int i = 0; i < FT; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j], af[i], acc[i][j], 0, 0, 0);
       }
     }
+  }
+
+  // The accumulators go through LDS as fp32 rows of the tile (padded by 16 bytes
+  // against bank conflicts), so that each thread finishes 8 consecutive columns
+  // with 16-byte loads and stores.
+  constexpr int LR = BN + 4;
+  static_assert(BT * LR * 4 <= tile_lds(BT, BN, NST, FP8), "the tile fits the stages' LDS");
+  float* tile = reinterpret_cast<float*>(lds);
+  wait_stage<0>();                                       // the stages have been read
+#pragma unroll
+  for (int i = 0; i < FT; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      *reinterpret_cast<f32x4_t*>(tile + ((wt * FT + i) * 16 + ln) * LR + (wn * FN + j) * 16 + q4) = acc[i][j];
+  __syncthreads();
+  constexpr int kChunks = NO / 8;
+  static_assert(BT * kChunks % (NW * 64) == 0, "every thread finishes as many chunks");
+#pragma unroll 1
+  for (int idx = threadIdx.x; idx < BT * kChunks; idx += NW * 64) {
+    const int r = idx / kChunks, c = (idx % kChunks) * 8;
+    const int64_t t = t0 + r;
+    const int n = n0 + c;
+    const bool in = t < a.T && n < a.N;
+    const float* p = tile + r * LR + (OP == DENSE_GLU ? (c >> 4) * 32 + (c & 15) : c);
+    float v[8];
+    *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(p);
+    *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(p + 4);
+    if constexpr (OP == DENSE_GLU) {
+      float u[8];
+      *reinterpret_cast<float4*>(u) = *reinterpret_cast<const float4*>(p + 16);
+      *reinterpret_cast<float4*>(u + 4) = *reinterpret_cast<const float4*>(p + 20);
+      finish_glu(a, t, n, in, v, u);
+    } else if constexpr (OP == DENSE_DGLU) {
+      if (in) finish_dglu(a, t, n, v);
+    } else {
+      if (in) finish_linear(a, t, n, v);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ matrix products of few rows
+//
+// At most 64 rows of A (a decode step's tokens): the weights are read once,
+// straight from memory into MFMA operands, and that stream bounds the kernel.
+// A wavefront takes 16 of the workgroup's weight rows (fragment rw of RW) and
+// every KW-th 128-byte step of k, U steps in flight; the KW partial sums meet in
+// LDS in a fixed order.  With few rows of A the MFMA's 16 x 16 block would be
+// mostly idle columns: P parts of k share it instead (16 / P weight rows and 16 / P
+// rows of A each, part p in rows and columns p * 16 / P ...; of the block only the
+// P diagonal squares are used).  That also makes the workgroups smaller and more
+// numerous.  A GLU's fragments alternate gate rows and the up rows of the same
+// columns.  e4m3 operands are widened to bf16: the matrix rate does not matter
+// here.
+template <DenseOp OP, int FP8, int RW, int KW, int P, int CT, int U>
+__global__ __launch_bounds__(RW * KW * 64) void dense_few_kernel(DenseArgs a) {
+  constexpr int NR = 16 / P;                              // weight rows per fragment, rows of A per column block
+  constexpr int NO = NR * RW / (OP == DENSE_GLU ? 2 : 1); // output columns of the workgroup
+  constexpr int ES = FP8 ? 1 : 2;
+  static_assert(P == 1 || CT == 1, "parts of k only where one column block holds the rows");
+  extern __shared__ __align__(16) char lds[];
+  f32x4_t* red = reinterpret_cast<f32x4_t*>(lds);         // [RW][KW][CT][64 lanes]
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rw = wave / KW, kw = wave % KW, q = lane >> 4, ln = lane & 15;
+  const int part = ln / NR, lr = ln % NR;
+  const int n0 = blockIdx.x * NO;
+  const int wn = min(n0 + (OP == DENSE_GLU ? rw / 2 * NR : rw * NR) + lr, a.N - 1);
+  const int64_t wrow = wn + (OP == DENSE_GLU && (rw & 1) ? (int64_t)a.N : 0);
+  const char* pw = static_cast<const char*>(a.b) + wrow * a.ldb * ES + 16 * q;
+  const char* px[CT];
+  int xt[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    xt[c] = min(16 * c + lr, a.T - 1);
+    px[c] = static_cast<const char*>(a.a) + xt[c] * a.lda * ES + 16 * q;
+  }
+  const int kb = a.K * ES;                                // bytes of a row
+  const int nk = (kb + 127) / 128;
+  const int scales_k = FP8 ? a.K / 128 : 0;
+  const float* sw = FP8 ? a.bs + wrow / 128 * scales_k : nullptr;
+  f32x4_t acc[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) acc[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  auto chunk = [&](const char* p, int at) {               // 16 bytes of this lane's row, zeros past its end
+    return at + 16 * q < kb ? *reinterpret_cast<const uint4*>(p + at) : make_uint4(0, 0, 0, 0);
+  };
+  for (int k0 = kw * P; k0 < nk; k0 += KW * P * U) {
+    uint4 w[U][2], x[U][CT][2];
+    float s[FP8 ? U : 1][CT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = (k0 + u * KW * P + part) * 128;
+      w[u][0] = chunk(pw, at);
+      w[u][1] = chunk(pw, at + 64);
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        x[u][c][0] = chunk(px[c], at);
+        x[u][c][1] = chunk(px[c], at + 64);
+        if constexpr (FP8) {
+          const int kk = at / 128;
+          s[u][c] = kk < nk ? a.as[(int64_t)xt[c] * scales_k + kk] * sw[kk] : 0.f;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        if constexpr (FP8) {
+          f32x4_t p = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t wd[4] = {w[u][h].x, w[u][h].y, w[u][h].z, w[u][h].w};
+            const uint32_t xd[4] = {x[u][c][h].x, x[u][c][h].y, x[u][c][h].z, x[u][c][h].w};
+#pragma unroll
+            for (int e = 0; e < 4; e += 2)
+              p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_e4m3(wd[e], wd[e + 1]), widen_e4m3(xd[e], xd[e + 1]), p,
+                                                          0, 0, 0);
+          }
+          // a lane's products belong to the k part of its column, and so does its scale; the weight rows'
+          // part is the same wherever the product is used
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[c][e] = __builtin_fmaf(p[e], s[u][c], acc[c][e]);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w[u][h]),
+                                                             __builtin_bit_cast(bf16x8_t, x[u][c][h]), acc[c], 0, 0, 0);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < CT; ++c) red[((rw * KW + kw) * CT + c) * 64 + lane] = acc[c];
+  __syncthreads();
+
+  // Four consecutive columns of one row per thread: their P parts of the KW sums.
+  constexpr int kChunks = NO / 4, kRows = CT * NR;
+  constexpr int kThreads = RW * KW * 64;
+  // whole groups of 32 threads stay together for the scale groups of 128 columns
+#pragma unroll 1
+  for (int idx = threadIdx.x; idx < kRows * kChunks; idx += kThreads) {
+    const int t = idx / kChunks, c4 = (idx % kChunks) * 4;
+    auto total = [&](int frag, int r4, float (&v)[4]) {   // rows r4 .. r4 + 3 of fragment `frag`
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = 0.f;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int row = p * NR + r4, col = p * NR + t % NR;
+        for (int w = 0; w < KW; ++w) {
+          const f32x4_t m = red[((frag * KW + w) * CT + t / NR) * 64 + (row / 4) * 16 + col];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] += m[e];
+        }
+      }
+    };
+    const int n = n0 + c4;
+    const bool in = t < a.T && n < a.N;
+    float v[4];
+    if constexpr (OP == DENSE_GLU) {
+      float u[4];
+      total(c4 / NR * 2, c4 % NR, v);
+      total(c4 / NR * 2 + 1, c4 % NR, u);
+      finish_glu(a, t, n, in, v, u);
+    } else {
+      total(c4 / NR, c4 % NR, v);
+      if (in) finish_linear(a, t, n, v);
+    }
+  }
+}
+
+namespace {
+
+template <DenseOp OP, int FP8, bool AK, bool BK, int WT, int WN, int FT, int FN, int NST>
+void launch_tile(const DenseArgs& a, hipStream_t s) {
+  constexpr int BT = WT * FT * 16, BN = WN * FN * 16, NO = OP == DENSE_GLU ? BN / 2 : BN;
+  constexpr size_t kLds = tile_lds(BT, BN, NST, FP8);
+  static_assert(kLds <= 160 * 1024, "LDS of one workgroup");
+  const int64_t tiles = (int64_t)((a.T + BT - 1) / BT) * ((a.N + NO - 1) / NO);
+  auto k = dense_tile_kernel<OP, FP8, AK, BK, WT, WN, FT, FN, NST>;
+  k<<<dim3((unsigned)tiles), WT * WN * 64, kLds, s>>>(a);
+}
+
+}  // namespace
+
+template <DenseOp OP, int FP8, int RW, int KW, int P, int CT, int U>
+static void launch_few_n(const DenseArgs& a, hipStream_t s) {
+  constexpr int NO = 16 / P * RW / (OP == DENSE_GLU ? 2 : 1);
+  constexpr size_t kLds = RW * KW * CT * 1024;
+  dense_few_kernel<OP, FP8, RW, KW, P, CT, U><<<dim3((a.N + NO - 1) / NO), RW * KW * 64, kLds, s>>>(a);
+}
+
+// At most 64 rows of A.  An e4m3 GLU output needs its 128 columns in one workgroup.
+template <DenseOp OP, int FP8>
+static void launch_few(const DenseArgs& a, hipStream_t s) {
+  constexpr int RW = OP == DENSE_GLU ? 2 : 1, KW = OP == DENSE_GLU ? 4 : 8;
+  if (OP == DENSE_GLU && a.hs) {
+    if constexpr (OP == DENSE_GLU) {
+      if (a.T <= 16) launch_few_n<OP, FP8, 16, 1, 1, 1, 4>(a, s);
+      else launch_few_n<OP, FP8, 16, 1, 1, 4, 1>(a, s);
+    }
+    return;
+  }
+  if (a.T <= 4) launch_few_n<OP, FP8, RW, KW, 4, 1, 4>(a, s);
+  else if (a.T <= 8) launch_few_n<OP, FP8, RW, KW, 2, 1, 4>(a, s);
+  else if (a.T <= 16) launch_few_n<OP, FP8, RW, KW, 1, 1, 4>(a, s);
+  else if (a.T <= 32) launch_few_n<OP, FP8, RW, KW, 1, 2, 2>(a, s);
+  else launch_few_n<OP, FP8, RW, KW, 1, 4, 2>(a, s);
+}
+
+template <DenseOp OP, int FP8, bool AK, bool BK>
+static void launch_sized(const DenseArgs& a, hipStream_t s) {
+  if constexpr (AK && BK && FP8 != 1) {
+    if (a.T <= 64) {
+      launch_few<OP, FP8>(a, s);
+      return;
+    }
+  }
+  if constexpr (OP == DENSE_GLU && FP8 != 1) {
+    if (a.hs) {                      // 128 output columns in one tile: a scale group
+      launch_tile<OP, FP8, AK, BK, 2, 4, 4, 4, 2>(a, s);
+      return;
+    }
+  }
+  auto tiles = [&](int side) {
+    return (int64_t)((a.T + side - 1) / side) * (((OP == DENSE_GLU ? 2 : 1) * (int64_t)a.N + side - 1) / side);
+  };
+  if (tiles(128) >= 256) {
+    if constexpr (FP8 || OP == DENSE_DGLU) launch_tile<OP, FP8, AK, BK, 2, 4, 4, 2, 2>(a, s);
+    else launch_tile<OP, FP8, AK, BK, 2, 2, 4, 4, 2>(a, s);
+  } else if (tiles(64) > 512) {
+    launch_tile<OP, FP8, AK, BK, 2, 2, 2, 2, 3>(a, s);
+  } else {
+    launch_tile<OP, FP8, AK, BK, 2, 2, 2, 2, 4>(a, s);
   }
 }
 
 void launch_dense(DenseOp op, bool fp8, bool ak, bool bk, const DenseArgs& a, hipStream_t s) {
-  const dim3 grid((a.N + 127) / 128, (a.T + 31) / 32);
-  if (op == DENSE_GLU && fp8) dense_kernel<DENSE_GLU, true, true, true><<<grid, 256, 0, s>>>(a);
-  else if (op == DENSE_GLU) dense_kernel<DENSE_GLU, false, true, true><<<grid, 256, 0, s>>>(a);
-  else if (op == DENSE_DGLU) dense_kernel<DENSE_DGLU, false, true, false><<<grid, 256, 0, s>>>(a);
-  else if (fp8) dense_kernel<DENSE_LINEAR, true, true, true><<<grid, 256, 0, s>>>(a);
-  else if (ak && bk) dense_kernel<DENSE_LINEAR, false, true, true><<<grid, 256, 0, s>>>(a);
-  else if (ak) dense_kernel<DENSE_LINEAR, false, true, false><<<grid, 256, 0, s>>>(a);
-  else dense_kernel<DENSE_LINEAR, false, false, false><<<grid, 256, 0, s>>>(a);
+  const bool wide = a.y_f32 || a.hs || a.T <= 64;        // e4m3 operands widened to bf16
+  if (op == DENSE_GLU && fp8 && wide) launch_sized<DENSE_GLU, 2, true, true>(a, s);
+  else if (op == DENSE_GLU && fp8) launch_sized<DENSE_GLU, 1, true, true>(a, s);
+  else if (op == DENSE_GLU) launch_sized<DENSE_GLU, 0, true, true>(a, s);
+  else if (op == DENSE_DGLU) launch_sized<DENSE_DGLU, 0, true, false>(a, s);
+  else if (fp8 && wide) launch_sized<DENSE_LINEAR, 2, true, true>(a, s);
+  else if (fp8) launch_sized<DENSE_LINEAR, 1, true, true>(a, s);
+  else if (ak && bk) launch_sized<DENSE_LINEAR, 0, true, true>(a, s);
+  else if (ak) launch_sized<DENSE_LINEAR, 0, true, false>(a, s);
+  else launch_sized<DENSE_LINEAR, 0, false, false>(a, s);
 }
 
 }  // namespace pe

@@ -26,10 +26,14 @@ struct Mat {
   }
 };
 
+// The products address the rows of one tile (256 of up to 2 bytes an element)
+// with 32-bit offsets from the tile's first.
+constexpr int64_t kMaxStride = 1 << 22;
+
 int check_mat(const Mat& m, bool optional) {
   if (!m.p) return optional ? PE_OK : fail(PE_ERR_INVALID_ARG, "%s is NULL", m.name);
-  if (m.ld < m.cols || m.ld > INT32_MAX)
-    return fail(PE_ERR_INVALID_ARG, "%s: row stride %lld outside [%lld, 2^31)", m.name, (long long)m.ld,
+  if (m.ld < m.cols || m.ld >= kMaxStride)
+    return fail(PE_ERR_INVALID_ARG, "%s: row stride %lld outside [%lld, 2^22)", m.name, (long long)m.ld,
                 (long long)m.cols);
   if ((uintptr_t)m.p % m.align || (m.rows > 1 && m.ld * m.es % m.align))
     return fail(PE_ERR_INVALID_ARG, "%s: address and row stride must be multiples of %d bytes", m.name, m.align);
@@ -103,7 +107,11 @@ int check_act(int act, bool none_ok) {
   return fail(PE_ERR_INVALID_ARG, "unknown activation %d", act);
 }
 
-bool vec4(const Mat& m) { return !m.p || ((uintptr_t)m.p % (4 * m.es) == 0 && m.ld % 4 == 0); }
+// Eight consecutive columns may be accessed as 16-byte vectors (8-byte ones of e4m3).
+bool vec8(const Mat& m) {
+  const int bytes = m.es == 1 ? 8 : 16;
+  return !m.p || ((uintptr_t)m.p % bytes == 0 && m.ld * m.es % bytes == 0);
+}
 
 }  // namespace
 
@@ -208,7 +216,7 @@ int pe_linear(int device, int wtype, const void* x, int64_t ldx, const float* xs
   a.bias = static_cast<const uint16_t*>(bias);
   a.residual = static_cast<const uint16_t*>(residual); a.ldr = ldr;
   a.y = y; a.ldy = ldy; a.y_f32 = ytype == PE_Y_FP32;
-  a.vec = vec4(my) && vec4(mr) && vec4({"", bias, 1, N, 4, 2, 2});
+  a.vec = vec8(my) && vec8(mr) && (uintptr_t)bias % 16 == 0;
   pe::launch_dense(pe::DENSE_LINEAR, fp8, true, true, a, static_cast<hipStream_t>(stream));
   PE_HIP(hipGetLastError());
   return PE_OK;
@@ -223,16 +231,15 @@ int pe_glu(int device, int wtype, int act, const void* x, int64_t ldx, const flo
   PE_TRY(check_wtype(wtype, H));
   PE_TRY(check_act(act, false));
   const bool fp8 = wtype == PE_W_FP8_B128;
-  if (I > INT32_MAX / 2) return fail(PE_ERR_INVALID_ARG, "inter=%d is too large", I);
   if ((fp8 || hscale) ? I % 128 : I % 8)
     return fail(PE_ERR_INVALID_ARG, "inter must be a multiple of %d", (fp8 || hscale) ? 128 : 8);
   if (T == 0) return PE_OK;
   const int es = fp8 ? 1 : 2, hs = hscale ? 1 : 2;
-  const Mat mx{"x", x, T, H, ldx, es, 16}, mw{"w13", w13, 2 * I, H, H, es, 16};
+  const Mat mx{"x", x, T, H, ldx, es, 16}, mw{"w13", w13, 2 * (int64_t)I, H, H, es, 16};
   const Mat mxs{"xscale", xscale, T, H / 128, H / 128, 4, 4};
-  const Mat mws{"s13", s13, 2 * (I / 128), H / 128, H / 128, 4, 4};
+  const Mat mws{"s13", s13, 2 * (int64_t)(I / 128), H / 128, H / 128, 4, 4};
   const Mat mh{"h", h, T, I, ldh, hs, hs}, mhs{"hscale", hscale, T, I / 128, I / 128, 4, 4};
-  const Mat mg{"gu", gu, T, 2 * I, 2 * I, 2, 16};
+  const Mat mg{"gu", gu, T, 2 * (int64_t)I, 2 * (int64_t)I, 2, 16};
   PE_TRY(check_mat(mx, false));
   PE_TRY(check_mat(mw, false));
   if (fp8) {
@@ -253,7 +260,7 @@ int pe_glu(int device, int wtype, int act, const void* x, int64_t ldx, const flo
   a.T = T; a.N = I; a.K = H; a.act = act;
   a.y = h; a.ldy = ldh; a.hs = hscale;
   a.gu = static_cast<uint16_t*>(gu);
-  a.vec = vec4(mh) && vec4(mg);
+  a.vec = vec8(mh);
   pe::launch_dense(pe::DENSE_GLU, fp8, true, true, a, static_cast<hipStream_t>(stream));
   PE_HIP(hipGetLastError());
   return PE_OK;
@@ -266,13 +273,13 @@ int pe_ffn_backward(int device, int act, const void* dy, int64_t lddy, const voi
   PE_TRY(check_dims(device, {H, I}));
   if (T < 0) return fail(PE_ERR_INVALID_ARG, "T=%d is negative", T);
   PE_TRY(check_act(act, false));
-  if (H % 8 || I % 8 || I > INT32_MAX / 2)
+  if (H % 8 || I % 8)
     return fail(PE_ERR_INVALID_ARG, "hidden and inter must be multiples of 8");
   if (!dx && !dw13 && !dw2) return fail(PE_ERR_INVALID_ARG, "no gradient is asked for");
-  const Mat mdy{"dy", dy, T, H, lddy, 2, 16}, mx{"x", x, T, H, ldx, 2, 16}, mgu{"gu", gu, T, 2 * I, 2 * I, 2, 16};
-  const Mat mw13{"w13", w13, 2 * I, H, H, 2, 16}, mw2{"w2", w2, H, I, I, 2, 16};
-  const Mat mdgu{"dgu", dgu, T, 2 * I, 2 * I, 2, 16}, mh{"h", h, T, I, I, 2, 16};
-  const Mat mdx{"dx", dx, T, H, lddx, 2, 16}, mdw13{"dw13", dw13, 2 * I, H, H, 2, 16}, mdw2{"dw2", dw2, H, I, I, 2, 16};
+  const Mat mdy{"dy", dy, T, H, lddy, 2, 16}, mx{"x", x, T, H, ldx, 2, 16}, mgu{"gu", gu, T, 2 * (int64_t)I, 2 * (int64_t)I, 2, 16};
+  const Mat mw13{"w13", w13, 2 * (int64_t)I, H, H, 2, 16}, mw2{"w2", w2, H, I, I, 2, 16};
+  const Mat mdgu{"dgu", dgu, T, 2 * (int64_t)I, 2 * (int64_t)I, 2, 16}, mh{"h", h, T, I, I, 2, 16};
+  const Mat mdx{"dx", dx, T, H, lddx, 2, 16}, mdw13{"dw13", dw13, 2 * (int64_t)I, H, H, 2, 16}, mdw2{"dw2", dw2, H, I, I, 2, 16};
   PE_TRY(check_mat(mdw13, true));
   PE_TRY(check_mat(mdw2, true));
   if (T > 0) {

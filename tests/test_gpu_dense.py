@@ -77,6 +77,18 @@ def _dev8(codes):
     return torch.from_numpy(codes).to(DEV).view(torch.float8_e4m3fn)
 
 
+def _aligned(x, w):
+    """The FP8 term of every sum_k x[t,k] w[n,k]: 7 * 2^-13 times the largest |product| of each eight k, added up."""
+    ax, aw = np.abs(x), np.abs(w)
+    total = np.zeros((x.shape[0], w.shape[0]))
+    for k in range(0, x.shape[1], 8):
+        m = np.zeros_like(total)
+        for j in range(k, k + 8):
+            np.maximum(m, np.outer(ax[:, j], aw[:, j]), out=m)
+        total += m
+    return 7 * 2.0 ** -13 * total
+
+
 def _within(got, ref, tol, what=""):
     bad = ~(np.abs(got - ref) <= tol)
     assert not bad.any(), "%s: %d of %d outside, first at %s: got %r, want %r +- %r" % (
@@ -219,6 +231,7 @@ def test_linear(T, N, K, fp8):
     bias, bv = _bf(rng.standard_normal(N))
     res, rv = _bf(rng.standard_normal((T, N)))
     mag = np.abs(xv) @ np.abs(wv).T
+    align = _aligned(xv, wv) if fp8 else 0.0
     args["x"] = _strided(args["x"])
     for act, with_bias, with_res, dt in [("none", False, False, torch.bfloat16), ("silu", True, True, torch.bfloat16),
                                          ("gelu", True, False, torch.float32), ("none", True, True, torch.float32),
@@ -235,7 +248,7 @@ def test_linear(T, N, K, fp8):
         pre = dense.linear(xv, wv, bv if with_bias else None, "none", None)
         y = dense.act(pre, act) + (rv if with_res else 0.0)
         # both activations change by at most 1.13 of their argument's change
-        err = 1.13 * (K + 8) * 2.0 ** -24 * (mag + np.abs(pre)) + FN * np.abs(dense.act(pre, act)) * (act != "none")
+        err = 1.13 * ((K + 8) * 2.0 ** -24 * (mag + np.abs(pre)) + align) + FN * np.abs(dense.act(pre, act)) * (act != "none")
         tol = err + (BF if dt == torch.bfloat16 else 2.0 ** -23) * (np.abs(y) + err) + 2.0 ** -24 * np.abs(pre)
         _within(_np(out), y, tol, "%s %s" % (act, dt))
         ok()
@@ -287,7 +300,7 @@ def test_glu(T, H, I, act, wtype, quant):
     args["x"] = _strided(args["x"])
     args["w13"] = args.pop("w")
     g, u, h = dense.glu(xv, wv, act)
-    mag = np.abs(xv) @ np.abs(wv).T * (H + 8) * 2.0 ** -24
+    mag = np.abs(xv) @ np.abs(wv).T * (H + 8) * 2.0 ** -24 + (_aligned(xv, wv) if fp8 else 0.0)
     dg, du = mag[:, :I], mag[:, I:]
     ag = np.abs(dense.act(g, act))
     err = (1.13 * dg + FN * ag) * (np.abs(u) + du) + ag * du + 2.0 ** -23 * np.abs(h)
@@ -559,11 +572,15 @@ def test_fp8_chain_through_the_shared_expert():
     torch.cuda.synchronize()
     qv, hv = dense.dequant_rows(_codes(q), _np(qs)), dense.dequant_rows(_codes(h), _np(hs))
     w13v, w2v = dense.dequant_blocks(c13, s13), dense.dequant_blocks(c2, s2)
-    _, _, href = dense.glu(qv, w13v, "silu")
-    # half an e4m3 step of each value, subnormal codes by their scale; the fp32 sums add far less than 1%
-    _within(hv, href, F8 * np.abs(href) * 1.01 + np.repeat(_np(hs), 128, 1) * 2.0 ** -9.9, "h")
+    g, u, href = dense.glu(qv, w13v, "silu")
+    # half an e4m3 step of each value, subnormal codes by their scale, and the products' own errors
+    e = (H + 8) * 2.0 ** -24 * (np.abs(qv) @ np.abs(w13v).T) + _aligned(qv, w13v)
+    ag = np.abs(dense.act(g, "silu"))
+    eh = (1.13 * e[:, :I] + FN * ag) * (np.abs(u) + e[:, I:]) + ag * e[:, I:]
+    _within(hv, href, F8 * (np.abs(href) + eh) * 1.001 + eh + np.repeat(_np(hs), 128, 1) * 2.0 ** -9.9, "h")
     yref = hv @ w2v.T + xv
-    tol = BF * np.abs(yref) + (I + 8) * 2.0 ** -24 * 2 * (np.abs(hv) @ np.abs(w2v).T + np.abs(xv))
+    tol = (I + 8) * 2.0 ** -24 * 2 * (np.abs(hv) @ np.abs(w2v).T + np.abs(xv)) + _aligned(hv, w2v)
+    tol = tol + BF * (np.abs(yref) + tol)
     _within(_np(y), yref, tol, "y")
 
 

@@ -28,7 +28,8 @@ def __getattr__(name):
     # The tensor functions of dense.py import torch, which the rest of the package does without.
     if name in ("rmsnorm", "route", "linear", "glu", "ffn_backward"):
         from . import dense
-        return getattr(dense, name)
+        globals().update((n, getattr(dense, n)) for n in ("rmsnorm", "route", "linear", "glu", "ffn_backward"))
+        return globals()[name]
     raise AttributeError("module %r has no attribute %r" % (__name__, name))
 
 

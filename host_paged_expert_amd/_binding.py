@@ -132,8 +132,9 @@ def _ptr(t):
         return None
     if isinstance(t, int):
         return t
-    if hasattr(t, "data_ptr"):
-        return t.data_ptr()
+    data_ptr = getattr(t, "data_ptr", None)
+    if data_ptr is not None:
+        return data_ptr()
     if hasattr(t, "ctypes"):
         return t.ctypes.data
     raise TypeError("cannot take a pointer of %r" % type(t))

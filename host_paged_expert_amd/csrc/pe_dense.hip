@@ -358,8 +358,9 @@ __device__ __forceinline__ bf16x8_t widen_e4m3(uint32_t lo, uint32_t hi) {
 template <int ROWS, int NW, bool KMAJOR>
 struct Operand {
   static constexpr int kInstr = ROWS / 8;               // 1024-byte copies per step
-  static constexpr int kPer = kInstr / NW;              // of which per wavefront
-  static_assert(kInstr % NW == 0 && NW % 2 == 0, "copies divide evenly");
+  static constexpr int kPer = (kInstr + NW - 1) / NW;   // of which per wavefront, at most
+  static constexpr int kMin = kInstr / NW;              // and at least
+  static_assert((kInstr % NW == 0 || kPer == 1) && NW % 2 == 0, "copies divide evenly, or go one each to the first");
 
   uint32_t off[kPer];     // K-major: byte offset of the lane's chunk from the tile's first row; k-slow: from row k0
   int kc[kPer];           // K-major: the chunk's byte within the 128; k-slow: its k row
@@ -388,20 +389,23 @@ struct Operand {
 
   static __device__ __forceinline__ int swz(int k) {
     if constexpr (ROWS >= 128) return (k & 3) | ((k >> 1) & 4);
-    return ((k >> 1) & 1) | ((k >> 2) & 2);
+    if constexpr (ROWS == 64) return ((k >> 1) & 1) | ((k >> 2) & 2);
+    return (k >> 3) & 1;
   }
 
   // Copy the step whose first chunk (or k row) is at `base`.
   __device__ __forceinline__ void copy(uint32_t lds, int wave, const char* base) const {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) copy_to_lds(lds + (wave + i * NW) * 1024, base, off[i]);
+    for (int i = 0; i < kPer; ++i)
+      if (kMin == kPer || wave < kInstr) copy_to_lds(lds + (wave + i * NW) * 1024, base, off[i]);
   }
   // The same where only the first `valid` bytes (k rows) of the step exist.
   __device__ __forceinline__ void copy_tail(uint32_t lds, int wave, const char* base, int valid) const {
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      copy_to_lds(lds + (wave + i * NW) * 1024,
-                  kc[i] < valid ? base + off[i] : reinterpret_cast<const char*>(g_zeros));
+      if (kMin == kPer || wave < kInstr)
+        copy_to_lds(lds + (wave + i * NW) * 1024,
+                    kc[i] < valid ? base + off[i] : reinterpret_cast<const char*>(g_zeros));
   }
 };
 
@@ -646,9 +650,10 @@ __global__ __launch_bounds__(WT * WN * 64) void dense_tile_kernel(DenseArgs a) {
       ob.copy_tail(st + kA, wave, pb + k * sb, BK ? tail * ES : tail);
     }
     if constexpr (FP8)
-      if (wave < BT / 64) copy_to_lds4(st + kA + kB + wave * 256, ps + k * 4);
+      if (wave * 64 < BT && (BT % 64 == 0 || lane < BT)) copy_to_lds4(st + kA + kB + wave * 256, ps + k * 4);
   };
-  constexpr int kCopies = decltype(oa)::kPer + decltype(ob)::kPer;     // per step (wavefronts with scales: one more)
+  // Copies per step of the wavefront with the fewest (waiting for that many more is waiting for enough).
+  constexpr int kCopies = decltype(oa)::kMin + decltype(ob)::kMin;
 
   f32x4_t acc[FT][FN];
 #pragma unroll
@@ -670,11 +675,11 @@ __global__ __launch_bounds__(WT * WN * 64) void dense_tile_kernel(DenseArgs a) {
   for (int k = 0; k < NST - 1; ++k)
     if (k < nk) fetch(k);
   for (int k = 0; k < nk; ++k) {
-    if (NST > 2 && k + NST - 2 < nk) wait_stage<(NST - 2) * kCopies>();
+    if (NST > 2 && k + NST - 1 <= nk) wait_stage<(NST - 2) * kCopies>();
     else wait_stage<0>();
     const char* st = lds + (k % NST) * kStage;
+    if (k + NST - 1 < nk) fetch(k + NST - 1);
     if constexpr (FP8) {
-      if (k + NST - 1 < nk) fetch(k + NST - 1);
       const float* sc = reinterpret_cast<const float*>(st + kA + kB) + wt * FT * 16 + ln;
       const float w0 = sw0[k], w1 = sw1[k];
       i32x8_t bf[FP8 == 1 ? FN : 1];
@@ -714,7 +719,6 @@ __global__ __launch_bounds__(WT * WN * 64) void dense_tile_kernel(DenseArgs a) {
         }
       }
     } else {
-      if (k + NST - 1 < nk) fetch(k + NST - 1);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         bf16x8_t af[FT], bf[FN];
@@ -745,7 +749,7 @@ __global__ __launch_bounds__(WT * WN * 64) void dense_tile_kernel(DenseArgs a) {
       *reinterpret_cast<f32x4_t*>(tile + ((wt * FT + i) * 16 + ln) * LR + (wn * FN + j) * 16 + q4) = acc[i][j];
   __syncthreads();
   constexpr int kChunks = NO / 8;
-  static_assert(BT * kChunks % (NW * 64) == 0, "every thread finishes as many chunks");
+  static_assert(BT * kChunks % 64 == 0, "whole wavefronts finish chunks: scale groups stay together");
 #pragma unroll 1
   for (int idx = threadIdx.x; idx < BT * kChunks; idx += NW * 64) {
     const int r = idx / kChunks, c = (idx % kChunks) * 8;
@@ -771,132 +775,115 @@ __global__ __launch_bounds__(WT * WN * 64) void dense_tile_kernel(DenseArgs a) {
 
 // ------------------------------------------------------------------ matrix products of few rows
 //
-// At most 64 rows of A (a decode step's tokens): the weights are read once,
-// straight from memory into MFMA operands, and that stream bounds the kernel.
-// A wavefront takes 16 of the workgroup's weight rows (fragment rw of RW) and
-// every KW-th 128-byte step of k, U steps in flight; the KW partial sums meet in
-// LDS in a fixed order.  With few rows of A the MFMA's 16 x 16 block would be
-// mostly idle columns: P parts of k share it instead (16 / P weight rows and 16 / P
-// rows of A each, part p in rows and columns p * 16 / P ...; of the block only the
-// P diagonal squares are used).  That also makes the workgroups smaller and more
-// numerous.  A GLU's fragments alternate gate rows and the up rows of the same
-// columns.  e4m3 operands are widened to bf16: the matrix rate does not matter
-// here.
-template <DenseOp OP, int FP8, int RW, int KW, int P, int CT, int U>
+// A few rows of A (a decode step's tokens): the weights' bytes bound the
+// product, so they stream straight from memory into MFMA operands, read once (by
+// each block of 16 rows of A).  A wavefront takes 16 of the workgroup's weight
+// rows (fragment rw of RW) and every KW-th 128-byte step of k, U steps in
+// flight; the KW partial sums meet in LDS in a fixed order.  With at most 8 rows of
+// A most columns of the MFMA's 16 x 16 block would be idle: P parts of k share it
+// instead (16 / P weight rows and 16 / P rows of A each, part p in rows and columns
+// p * 16 / P ...; of the block only the P diagonal squares are used).  One compute
+// unit cannot draw more than some 55 GB/s from memory, so what counts is that the
+// smaller workgroups are P times as many: gate/up 2 x 6144 x 2048 in bf16 for one
+// row, 10.1 us (5.0 TB/s) with P = 4 against 12-14 us with P = 1.  A GLU's fragments
+// alternate gate rows and the up rows of the same columns.
+template <DenseOp OP, int FP8, int RW, int KW, int P, int U>
 __global__ __launch_bounds__(RW * KW * 64) void dense_few_kernel(DenseArgs a) {
-  constexpr int NR = 16 / P;                              // weight rows per fragment, rows of A per column block
+  constexpr int NR = 16 / P;                              // weight rows per fragment, rows of A per workgroup
   constexpr int NO = NR * RW / (OP == DENSE_GLU ? 2 : 1); // output columns of the workgroup
   constexpr int ES = FP8 ? 1 : 2;
-  static_assert(P == 1 || CT == 1, "parts of k only where one column block holds the rows");
-  extern __shared__ __align__(16) char lds[];
-  f32x4_t* red = reinterpret_cast<f32x4_t*>(lds);         // [RW][KW][CT][64 lanes]
+  __shared__ f32x4_t red[RW][KW][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rw = wave / KW, kw = wave % KW, q = lane >> 4, ln = lane & 15;
   const int part = ln / NR, lr = ln % NR;
-  const int n0 = blockIdx.x * NO;
+  const int n0 = blockIdx.x * NO, t0 = blockIdx.y * NR;
   const int wn = min(n0 + (OP == DENSE_GLU ? rw / 2 * NR : rw * NR) + lr, a.N - 1);
   const int64_t wrow = wn + (OP == DENSE_GLU && (rw & 1) ? (int64_t)a.N : 0);
+  const int64_t xrow = min(t0 + lr, a.T - 1);
   const char* pw = static_cast<const char*>(a.b) + wrow * a.ldb * ES + 16 * q;
-  const char* px[CT];
-  int xt[CT];
-#pragma unroll
-  for (int c = 0; c < CT; ++c) {
-    xt[c] = min(16 * c + lr, a.T - 1);
-    px[c] = static_cast<const char*>(a.a) + xt[c] * a.lda * ES + 16 * q;
-  }
+  const char* px = static_cast<const char*>(a.a) + xrow * a.lda * ES + 16 * q;
   const int kb = a.K * ES;                                // bytes of a row
   const int nk = (kb + 127) / 128;
   const int scales_k = FP8 ? a.K / 128 : 0;
   const float* sw = FP8 ? a.bs + wrow / 128 * scales_k : nullptr;
-  f32x4_t acc[CT];
-#pragma unroll
-  for (int c = 0; c < CT; ++c) acc[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const float* sx = FP8 ? a.as + xrow * scales_k : nullptr;
+  f32x4_t acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
   auto chunk = [&](const char* p, int at) {               // 16 bytes of this lane's row, zeros past its end
     return at + 16 * q < kb ? *reinterpret_cast<const uint4*>(p + at) : make_uint4(0, 0, 0, 0);
   };
   for (int k0 = kw * P; k0 < nk; k0 += KW * P * U) {
-    uint4 w[U][2], x[U][CT][2];
-    float s[FP8 ? U : 1][CT];
+    uint4 w[U][2], x[U][2];
+    float s[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int at = (k0 + u * KW * P + part) * 128;
+      const int k = k0 + u * KW * P + part, at = k * 128;
       w[u][0] = chunk(pw, at);
       w[u][1] = chunk(pw, at + 64);
-#pragma unroll
-      for (int c = 0; c < CT; ++c) {
-        x[u][c][0] = chunk(px[c], at);
-        x[u][c][1] = chunk(px[c], at + 64);
-        if constexpr (FP8) {
-          const int kk = at / 128;
-          s[u][c] = kk < nk ? a.as[(int64_t)xt[c] * scales_k + kk] * sw[kk] : 0.f;
-        }
-      }
+      x[u][0] = chunk(px, at);
+      x[u][1] = chunk(px, at + 64);
+      // a lane's products belong to the k part of its column, and so does its scale; every weight row of
+      // the fragment lies in one scale block
+      if constexpr (FP8) s[u] = k < nk ? sx[k] * sw[k] : 0.f;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      const uint32_t wd[8] = {w[u][0].x, w[u][0].y, w[u][0].z, w[u][0].w, w[u][1].x, w[u][1].y, w[u][1].z, w[u][1].w};
+      const uint32_t xd[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
+      if constexpr (FP8) {
+        f32x4_t p = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        if constexpr (FP8 == 1) {
+          i32x8_t wv, xv;
 #pragma unroll
-      for (int c = 0; c < CT; ++c) {
-        if constexpr (FP8) {
-          f32x4_t p = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t wd[4] = {w[u][h].x, w[u][h].y, w[u][h].z, w[u][h].w};
-            const uint32_t xd[4] = {x[u][c][h].x, x[u][c][h].y, x[u][c][h].z, x[u][c][h].w};
-#pragma unroll
-            for (int e = 0; e < 4; e += 2)
-              p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_e4m3(wd[e], wd[e + 1]), widen_e4m3(xd[e], xd[e + 1]), p,
-                                                          0, 0, 0);
-          }
-          // a lane's products belong to the k part of its column, and so does its scale; the weight rows'
-          // part is the same wherever the product is used
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[c][e] = __builtin_fmaf(p[e], s[u][c], acc[c][e]);
+          for (int e = 0; e < 8; ++e) { wv[e] = (int)wd[e]; xv[e] = (int)xd[e]; }
+          p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, xv, p, 0, 0, 0, 0, 0, 0);   // no block scales
         } else {
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w[u][h]),
-                                                             __builtin_bit_cast(bf16x8_t, x[u][c][h]), acc[c], 0, 0, 0);
+          for (int e = 0; e < 8; e += 2)
+            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_e4m3(wd[e], wd[e + 1]), widen_e4m3(xd[e], xd[e + 1]), p,
+                                                        0, 0, 0);
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(p[e], s[u], acc[e]);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w[u][h]),
+                                                        __builtin_bit_cast(bf16x8_t, x[u][h]), acc, 0, 0, 0);
       }
     }
   }
-#pragma unroll
-  for (int c = 0; c < CT; ++c) red[((rw * KW + kw) * CT + c) * 64 + lane] = acc[c];
+  red[rw][kw][lane] = acc;
   __syncthreads();
 
   // Four consecutive columns of one row per thread: their P parts of the KW sums.
-  constexpr int kChunks = NO / 4, kRows = CT * NR;
-  constexpr int kThreads = RW * KW * 64;
-  // whole groups of 32 threads stay together for the scale groups of 128 columns
-#pragma unroll 1
-  for (int idx = threadIdx.x; idx < kRows * kChunks; idx += kThreads) {
-    const int t = idx / kChunks, c4 = (idx % kChunks) * 4;
-    auto total = [&](int frag, int r4, float (&v)[4]) {   // rows r4 .. r4 + 3 of fragment `frag`
+  constexpr int kChunks = NO / 4;
+  if (threadIdx.x >= NR * kChunks) return;
+  const int tr = threadIdx.x / kChunks, c4 = (threadIdx.x % kChunks) * 4;
+  auto total = [&](int frag, int r4, float (&v)[4]) {     // rows r4 .. r4 + 3 of fragment `frag`
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = 0.f;
+    for (int e = 0; e < 4; ++e) v[e] = 0.f;
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int row = p * NR + r4, col = p * NR + t % NR;
-        for (int w = 0; w < KW; ++w) {
-          const f32x4_t m = red[((frag * KW + w) * CT + t / NR) * 64 + (row / 4) * 16 + col];
+    for (int p = 0; p < P; ++p)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] += m[e];
-        }
+      for (int w = 0; w < KW; ++w) {
+        const f32x4_t m = red[frag][w][(p * NR + r4) / 4 * 16 + p * NR + tr];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += m[e];
       }
-    };
-    const int n = n0 + c4;
-    const bool in = t < a.T && n < a.N;
-    float v[4];
-    if constexpr (OP == DENSE_GLU) {
-      float u[4];
-      total(c4 / NR * 2, c4 % NR, v);
-      total(c4 / NR * 2 + 1, c4 % NR, u);
-      finish_glu(a, t, n, in, v, u);
-    } else {
-      total(c4 / NR, c4 % NR, v);
-      if (in) finish_linear(a, t, n, v);
-    }
+  };
+  const int64_t t = t0 + tr;
+  const int n = n0 + c4;
+  if (t >= a.T || n >= a.N) return;
+  float v[4];
+  if constexpr (OP == DENSE_GLU) {
+    float u[4];
+    total(c4 / NR * 2, c4 % NR, v);
+    total(c4 / NR * 2 + 1, c4 % NR, u);
+    finish_glu(a, t, n, true, v, u);
+  } else {
+    total(c4 / NR, c4 % NR, v);
+    finish_linear(a, t, n, v);
   }
 }
 
@@ -914,60 +901,56 @@ void launch_tile(const DenseArgs& a, hipStream_t s) {
 
 }  // namespace
 
-template <DenseOp OP, int FP8, int RW, int KW, int P, int CT, int U>
+template <DenseOp OP, int FP8, int RW, int KW, int P, int U>
 static void launch_few_n(const DenseArgs& a, hipStream_t s) {
-  constexpr int NO = 16 / P * RW / (OP == DENSE_GLU ? 2 : 1);
-  constexpr size_t kLds = RW * KW * CT * 1024;
-  dense_few_kernel<OP, FP8, RW, KW, P, CT, U><<<dim3((a.N + NO - 1) / NO), RW * KW * 64, kLds, s>>>(a);
-}
-
-// At most 64 rows of A.  An e4m3 GLU output needs its 128 columns in one workgroup.
-template <DenseOp OP, int FP8>
-static void launch_few(const DenseArgs& a, hipStream_t s) {
-  constexpr int RW = OP == DENSE_GLU ? 2 : 1, KW = OP == DENSE_GLU ? 4 : 8;
-  if (OP == DENSE_GLU && a.hs) {
-    if constexpr (OP == DENSE_GLU) {
-      if (a.T <= 16) launch_few_n<OP, FP8, 16, 1, 1, 1, 4>(a, s);
-      else launch_few_n<OP, FP8, 16, 1, 1, 4, 1>(a, s);
-    }
-    return;
-  }
-  if (a.T <= 4) launch_few_n<OP, FP8, RW, KW, 4, 1, 4>(a, s);
-  else if (a.T <= 8) launch_few_n<OP, FP8, RW, KW, 2, 1, 4>(a, s);
-  else if (a.T <= 16) launch_few_n<OP, FP8, RW, KW, 1, 1, 4>(a, s);
-  else if (a.T <= 32) launch_few_n<OP, FP8, RW, KW, 1, 2, 2>(a, s);
-  else launch_few_n<OP, FP8, RW, KW, 1, 4, 2>(a, s);
+  constexpr int NR = 16 / P, NO = NR * RW / (OP == DENSE_GLU ? 2 : 1);
+  dense_few_kernel<OP, FP8, RW, KW, P, U><<<dim3((a.N + NO - 1) / NO, (a.T + NR - 1) / NR), RW * KW * 64, 0, s>>>(a);
 }
 
 template <DenseOp OP, int FP8, bool AK, bool BK>
 static void launch_sized(const DenseArgs& a, hipStream_t s) {
-  if constexpr (AK && BK && FP8 != 1) {
-    if (a.T <= 64) {
-      launch_few<OP, FP8>(a, s);
-      return;
-    }
-  }
+  auto tiles = [&](int bt, int bn) {
+    return (int64_t)((a.T + bt - 1) / bt) * (((OP == DENSE_GLU ? 2 : 1) * (int64_t)a.N + bn - 1) / bn);
+  };
   if constexpr (OP == DENSE_GLU && FP8 != 1) {
     if (a.hs) {                      // 128 output columns in one tile: a scale group
-      launch_tile<OP, FP8, AK, BK, 2, 4, 4, 4, 2>(a, s);
+      if (tiles(16, 256) <= 256) launch_tile<OP, FP8, AK, BK, 1, 8, 1, 2, 4>(a, s);
+      else if (tiles(32, 256) <= 256) launch_tile<OP, FP8, AK, BK, 1, 8, 2, 2, 4>(a, s);
+      else if (tiles(64, 256) <= 256) launch_tile<OP, FP8, AK, BK, 1, 8, 4, 2, 3>(a, s);
+      else launch_tile<OP, FP8, AK, BK, 2, 4, 4, 4, 2>(a, s);
       return;
     }
   }
-  auto tiles = [&](int side) {
-    return (int64_t)((a.T + side - 1) / side) * (((OP == DENSE_GLU ? 2 : 1) * (int64_t)a.N + side - 1) / side);
-  };
-  if (tiles(128) >= 256) {
-    if constexpr (FP8 || OP == DENSE_DGLU) launch_tile<OP, FP8, AK, BK, 2, 4, 4, 2, 2>(a, s);
+  if constexpr (AK && BK) {
+    constexpr bool GLU = OP == DENSE_GLU;
+    if (a.T <= 4) {
+      launch_few_n<OP, FP8, GLU ? 2 : 1, GLU ? 2 : 8, 4, 4>(a, s);
+      return;
+    }
+    if (a.T <= 8) {
+      launch_few_n<OP, FP8, GLU ? 2 : 1, GLU ? 4 : 8, 2, 4>(a, s);
+      return;
+    }
+    if (a.T <= 64 && tiles(64, 64) < 128) {
+      launch_few_n<OP, FP8, GLU ? 2 : 1, GLU ? 4 : 8, 1, 4>(a, s);
+      return;
+    }
+  }
+  if (tiles(128, 128) >= 256) {
+    if constexpr (FP8 != 0) launch_tile<OP, FP8, AK, BK, 4, 2, 2, 4, 2>(a, s);
+    else if constexpr (OP == DENSE_DGLU) launch_tile<OP, FP8, AK, BK, 2, 4, 4, 2, 2>(a, s);
     else launch_tile<OP, FP8, AK, BK, 2, 2, 4, 4, 2>(a, s);
-  } else if (tiles(64) > 512) {
-    launch_tile<OP, FP8, AK, BK, 2, 2, 2, 2, 3>(a, s);
-  } else {
+  } else if (tiles(64, 64) > 256) {
+    launch_tile<OP, FP8, AK, BK, 2, 2, 2, 2, 2>(a, s);
+  } else if (tiles(64, 64) > 128) {
     launch_tile<OP, FP8, AK, BK, 2, 2, 2, 2, 4>(a, s);
+  } else {
+    launch_tile<OP, FP8, AK, BK, 2, 2, 1, OP == DENSE_GLU ? 2 : 1, 4>(a, s);
   }
 }
 
 void launch_dense(DenseOp op, bool fp8, bool ak, bool bk, const DenseArgs& a, hipStream_t s) {
-  const bool wide = a.y_f32 || a.hs || a.T <= 64;        // e4m3 operands widened to bf16
+  const bool wide = a.y_f32 || a.hs;                     // e4m3 operands widened to bf16
   if (op == DENSE_GLU && fp8 && wide) launch_sized<DENSE_GLU, 2, true, true>(a, s);
   else if (op == DENSE_GLU && fp8) launch_sized<DENSE_GLU, 1, true, true>(a, s);
   else if (op == DENSE_GLU) launch_sized<DENSE_GLU, 0, true, true>(a, s);

@@ -20,6 +20,11 @@ _E4M3 = (torch.float8_e4m3fn, torch.uint8)
 
 def _mat(name, t, dtypes, shape, dev, strided=False):
     """Raise unless `t` is a matrix (or vector) of this shape, type and device; its row stride."""
+    try:
+        if t.shape == shape and t.dtype in dtypes and t.device == dev and t.is_contiguous():
+            return shape[-1]
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
     if t.dtype not in dtypes or t.device != dev:
@@ -27,16 +32,14 @@ def _mat(name, t, dtypes, shape, dev, strided=False):
             name, " or ".join(str(d) for d in dtypes), dev, t.dtype, t.device))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if strided and len(shape) == 2:
-        row, col = t.stride()
-        if shape[0] <= 1:                 # the stride of a single row is any number
-            row = shape[1]
-        if (col != 1 and shape[1] > 1) or row < shape[1]:
-            raise ValueError("%s must have contiguous rows that do not overlap (strides %s)" % (name, t.stride()))
-        return row
-    if not t.is_contiguous():
+    if not strided or len(shape) != 2:
         raise ValueError("%s must be contiguous" % name)
-    return shape[-1]
+    row, col = t.stride()
+    if shape[0] <= 1:                     # the stride of a single row is any number
+        row = shape[1]
+    if (col != 1 and shape[1] > 1) or row < shape[1]:
+        raise ValueError("%s must have contiguous rows that do not overlap (strides %s)" % (name, t.stride()))
+    return row
 
 
 def _left(name, t):

@@ -148,6 +148,9 @@ def _stream(s):
     return s.cuda_stream
 
 
+check, stream_handle = _check, _stream      # for dense.py, which marshals its tensors itself
+
+
 # ---------------------------------------------------------------- entry points
 
 def pe_create(num_layers, num_experts, top_k, num_resident, hidden, inter, max_tokens, wtype="bf16",

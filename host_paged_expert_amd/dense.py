@@ -14,24 +14,31 @@ import torch
 
 from . import _binding as b
 
-_BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
 
 
-def _mat(name, t, dtypes, shape, dev, strided=False):
-    """Raise unless `t` is a matrix (or vector) of this shape, type and device; its row stride."""
+def _plain(t, dtype, shape, d):
+    """Whether `t` is a contiguous tensor of this type and shape on GPU `d`: the common case, told quickly.  A decode
+    step's calls take a few microseconds each, and this is most of what Python adds to them."""
     try:
-        if t.shape == shape and t.dtype in dtypes and t.device == dev and t.is_contiguous():
-            return shape[-1]
-    except AttributeError:
-        pass
+        return t.shape == shape and t.dtype is dtype and t.get_device() == d and t.is_contiguous()
+    except (AttributeError, TypeError):
+        return False
+
+
+def _mat(name, t, dtypes, shape, d, strided=False):
+    """Raise unless `t` is a matrix (or vector) of this shape, type and device; its row stride."""
+    dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
-    if t.dtype not in dtypes or t.device != dev:
-        raise ValueError("%s must be a %s tensor on %s (got %s on %s)" % (
-            name, " or ".join(str(d) for d in dtypes), dev, t.dtype, t.device))
+    if t.dtype not in dtypes or t.get_device() != d:
+        raise ValueError("%s must be a %s tensor on cuda:%d (got %s on %s)" % (
+            name, " or ".join(str(k) for k in dtypes), d, t.dtype, t.device))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.is_contiguous():
+        return shape[-1]
     if not strided or len(shape) != 2:
         raise ValueError("%s must be contiguous" % name)
     row, col = t.stride()
@@ -42,17 +49,30 @@ def _mat(name, t, dtypes, shape, dev, strided=False):
     return row
 
 
+def _ld(name, t, dtype, shape, d):
+    """Row stride of a matrix whose rows may lie apart."""
+    return shape[1] if _plain(t, dtype, shape, d) else _mat(name, t, dtype, shape, d, True)
+
+
+def _need(name, t, dtype, shape, d):
+    """Address of a contiguous tensor, or of none if it is optional and absent."""
+    if not _plain(t, dtype, shape, d):
+        _mat(name, t, dtype, shape, d)
+    return t.data_ptr()
+
+
+def _opt(name, t, dtype, shape, d):
+    return None if t is None else _need(name, t, dtype, shape, d)
+
+
 def _left(name, t):
-    """Shape and device of the operand the others are checked against."""
+    """Shape and GPU of the operand the others are checked against."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
-    if t.dim() != 2 or t.device.type != "cuda":
+    if not t.is_cuda or t.dim() != 2:
         raise ValueError("%s must be a matrix on the GPU (got shape %s on %s)" % (name, tuple(t.shape), t.device))
-    return t.shape[0], t.shape[1], t.device
-
-
-def _opt(name, t, dtypes, shape, dev, strided=False):
-    return 0 if t is None else _mat(name, t, dtypes, shape, dev, strided)
+    T, C = t.shape
+    return T, C, t.get_device()
 
 
 def _choice(name, value, table):
@@ -64,39 +84,48 @@ def _choice(name, value, table):
 def rmsnorm(x, weight, eps, out, scales=None, residual=None, sum_out=None, stream=None):
     """out = rms_norm(x + residual) * weight as bf16, or as e4m3 codes with `scales`
     fp32 [T, H/128]; sum_out (optional) = x + residual as bf16."""
-    T, H, dev = _left("x", x)
-    ldx = _mat("x", x, _BF16, (T, H), dev, True)
-    _mat("weight", weight, _BF16, (H,), dev)
-    ldr = _opt("residual", residual, _BF16, (T, H), dev, True)
-    lds = _opt("sum_out", sum_out, _BF16, (T, H), dev, True)
-    ldy = _mat("out", out, _BF16 if scales is None else _E4M3, (T, H), dev, True)
-    _opt("scales", scales, _F32, (T, H // 128), dev)
-    return b.pe_rmsnorm(dev.index, x, ldx, residual, ldr, weight, eps, T, H, sum_out, lds, out, ldy, scales, stream)
+    T, H, d = _left("x", x)
+    shape = (T, H)
+    ldx = _ld("x", x, _BF16, shape, d)
+    ldr = lds = 0
+    r = s = None
+    if residual is not None:
+        ldr, r = _ld("residual", residual, _BF16, shape, d), residual.data_ptr()
+    if sum_out is not None:
+        lds, s = _ld("sum_out", sum_out, _BF16, shape, d), sum_out.data_ptr()
+    w = _need("weight", weight, _BF16, (H,), d)
+    if scales is None:
+        ldy, q = _ld("out", out, _BF16, shape, d), None
+    else:
+        ldy = H if _plain(out, _E4M3[0], shape, d) else _mat("out", out, _E4M3, shape, d, True)
+        q = _need("scales", scales, _F32, (T, H // 128), d)
+    return b.check(b.lib().pe_rmsnorm(d, x.data_ptr(), ldx, r, ldr, w, eps, T, H, s, lds, out.data_ptr(), ldy, q,
+                                      b.stream_handle(stream)))
 
 
 def route(logits, topk_ids, topk_w, scoring="softmax", renormalize=True, scale=1.0, stream=None):
     """Top-k ids (int32 [T, k]) and weights (fp32 [T, k]) of fp32 logits [T, E], for PagedMoE.forward."""
-    T, E, dev = _left("logits", logits)
-    ldl = _mat("logits", logits, _F32, (T, E), dev, True)
+    T, E, d = _left("logits", logits)
+    ldl = _ld("logits", logits, _F32, (T, E), d)
     if not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != 2:
         raise ValueError("topk_ids must be a [T, k] tensor")
     k = topk_ids.shape[1]
-    _mat("topk_ids", topk_ids, _I32, (T, k), dev)
-    _mat("topk_w", topk_w, _F32, (T, k), dev)
-    return b.pe_route(dev.index, logits, ldl, T, E, k, _choice("scoring", scoring, b.SCORES), renormalize, scale,
-                      topk_ids, topk_w, stream)
+    ids = _need("topk_ids", topk_ids, _I32, (T, k), d)
+    w = _need("topk_w", topk_w, _F32, (T, k), d)
+    return b.check(b.lib().pe_route(d, logits.data_ptr(), ldl, T, E, k, _choice("scoring", scoring, b.SCORES),
+                                    1 if renormalize else 0, scale, ids, w, b.stream_handle(stream)))
 
 
 def _operands(x, w, x_scales, w_scales, w_rows):
-    """Checks of a product's operands: (T, K, device, weight format, x's row stride)."""
-    T, K, dev = _left("x", x)
-    fp8 = x_scales is not None or w_scales is not None
-    ld = _mat("x", x, _E4M3 if fp8 else _BF16, (T, K), dev, True)
-    _mat("w", w, _E4M3 if fp8 else _BF16, (w_rows, K), dev)
-    if fp8:
-        _mat("x_scales", x_scales, _F32, (T, K // 128), dev)
-        _mat("w_scales", w_scales, _F32, (-(-w_rows // 128), K // 128), dev)
-    return T, K, dev, b.PE_W_FP8_B128 if fp8 else b.PE_W_BF16, ld
+    """Checks of a product's operands: T, K, GPU, weight format, x's row stride, addresses of w and the scales."""
+    T, K, d = _left("x", x)
+    if x_scales is None and w_scales is None:
+        return (T, K, d, b.PE_W_BF16, _ld("x", x, _BF16, (T, K), d), _need("w", w, _BF16, (w_rows, K), d), None, None)
+    ld = K if _plain(x, _E4M3[0], (T, K), d) else _mat("x", x, _E4M3, (T, K), d, True)
+    if not _plain(w, _E4M3[0], (w_rows, K), d):
+        _mat("w", w, _E4M3, (w_rows, K), d)
+    return (T, K, d, b.PE_W_FP8_B128, ld, w.data_ptr(), _need("x_scales", x_scales, _F32, (T, K // 128), d),
+            _need("w_scales", w_scales, _F32, (-(-w_rows // 128), K // 128), d))
 
 
 def linear(x, w, out, x_scales=None, w_scales=None, bias=None, act="none", residual=None, stream=None):
@@ -105,12 +134,20 @@ def linear(x, w, out, x_scales=None, w_scales=None, bias=None, act="none", resid
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("w must be a [N, K] tensor")
     N = w.shape[0]
-    T, K, dev, wtype, ldx = _operands(x, w, x_scales, w_scales, N)
-    _opt("bias", bias, _BF16, (N,), dev)
-    ldr = _opt("residual", residual, _BF16, (T, N), dev, True)
-    ldy = _mat("out", out, _BF16 + _F32, (T, N), dev, True)
-    return b.pe_linear(dev.index, wtype, x, ldx, x_scales, w, w_scales, bias, _choice("act", act, b.ACTS), residual,
-                       ldr, T, N, K, out, ldy, b.PE_Y_FP32 if out.dtype is torch.float32 else b.PE_Y_BF16, stream)
+    T, K, d, wtype, ldx, wp, xs, ws = _operands(x, w, x_scales, w_scales, N)
+    bp = _opt("bias", bias, _BF16, (N,), d)
+    ldr, r = 0, None
+    if residual is not None:
+        ldr, r = _ld("residual", residual, _BF16, (T, N), d), residual.data_ptr()
+    ytype = b.PE_Y_BF16
+    if _plain(out, _BF16, (T, N), d):
+        ldy = N
+    else:
+        ldy = _mat("out", out, (_BF16, _F32), (T, N), d, True)
+        if out.dtype is _F32:
+            ytype = b.PE_Y_FP32
+    return b.check(b.lib().pe_linear(d, wtype, x.data_ptr(), ldx, xs, wp, ws, bp, _choice("act", act, b.ACTS), r, ldr,
+                                     T, N, K, out.data_ptr(), ldy, ytype, b.stream_handle(stream)))
 
 
 def glu(x, w13, out, x_scales=None, w_scales=None, out_scales=None, act="silu", gu=None, stream=None):
@@ -119,30 +156,33 @@ def glu(x, w13, out, x_scales=None, w_scales=None, out_scales=None, act="silu", 
     if not isinstance(out, torch.Tensor) or out.dim() != 2:
         raise ValueError("out must be a [T, I] tensor")
     I = out.shape[1]
-    T, H, dev, wtype, ldx = _operands(x, w13, x_scales, w_scales, 2 * I)
-    ldh = _mat("out", out, _BF16 if out_scales is None else _E4M3, (T, I), dev, True)
-    _opt("out_scales", out_scales, _F32, (T, I // 128), dev)
-    _opt("gu", gu, _BF16, (T, 2 * I), dev)
-    return b.pe_glu(dev.index, wtype, _choice("act", act, b.ACTS), x, ldx, x_scales, w13, w_scales, T, H, I, out, ldh,
-                    out_scales, gu, stream)
+    T, H, d, wtype, ldx, wp, xs, ws = _operands(x, w13, x_scales, w_scales, 2 * I)
+    if out_scales is None:
+        ldh, hs = _ld("out", out, _BF16, (T, I), d), None
+    else:
+        ldh = I if _plain(out, _E4M3[0], (T, I), d) else _mat("out", out, _E4M3, (T, I), d, True)
+        hs = _need("out_scales", out_scales, _F32, (T, I // 128), d)
+    return b.check(b.lib().pe_glu(d, wtype, _choice("act", act, b.ACTS), x.data_ptr(), ldx, xs, wp, ws, T, H, I,
+                                  out.data_ptr(), ldh, hs, _opt("gu", gu, _BF16, (T, 2 * I), d),
+                                  b.stream_handle(stream)))
 
 
 def ffn_backward(dy, x, gu, w13, w2, dgu, h=None, dx=None, dw13=None, dw2=None, act="silu", stream=None):
     """Gradients of y = glu(x, w13) w2^T for dy: whichever of dx, dw13, dw2 (bf16) are given.
     gu is glu's kept output; dgu [T, 2I] and (with dw2) h [T, I] are written on the way."""
-    T, H, dev = _left("dy", dy)
+    T, H, d = _left("dy", dy)
     if not isinstance(w2, torch.Tensor) or w2.dim() != 2:
         raise ValueError("w2 must be a [H, I] tensor")
     I = w2.shape[1]
-    lddy = _mat("dy", dy, _BF16, (T, H), dev, True)
-    ldx = _opt("x", x, _BF16, (T, H), dev, True)
-    _mat("gu", gu, _BF16, (T, 2 * I), dev)
-    _opt("w13", w13, _BF16, (2 * I, H), dev)
-    _mat("w2", w2, _BF16, (H, I), dev)
-    _mat("dgu", dgu, _BF16, (T, 2 * I), dev)
-    _opt("h", h, _BF16, (T, I), dev)
-    lddx = _opt("dx", dx, _BF16, (T, H), dev, True)
-    _opt("dw13", dw13, _BF16, (2 * I, H), dev)
-    _opt("dw2", dw2, _BF16, (H, I), dev)
-    return b.pe_ffn_backward(dev.index, _choice("act", act, b.ACTS), dy, lddy, x, ldx, gu, w13, w2, T, H, I, dgu, h, dx,
-                             lddx, dw13, dw2, stream)
+    lddy = _ld("dy", dy, _BF16, (T, H), d)
+    ldx = lddx = 0
+    xp = dxp = None
+    if x is not None:
+        ldx, xp = _ld("x", x, _BF16, (T, H), d), x.data_ptr()
+    if dx is not None:
+        lddx, dxp = _ld("dx", dx, _BF16, (T, H), d), dx.data_ptr()
+    return b.check(b.lib().pe_ffn_backward(
+        d, _choice("act", act, b.ACTS), dy.data_ptr(), lddy, xp, ldx, _need("gu", gu, _BF16, (T, 2 * I), d),
+        _opt("w13", w13, _BF16, (2 * I, H), d), _need("w2", w2, _BF16, (H, I), d),
+        T, H, I, _need("dgu", dgu, _BF16, (T, 2 * I), d), _opt("h", h, _BF16, (T, I), d), dxp, lddx,
+        _opt("dw13", dw13, _BF16, (2 * I, H), d), _opt("dw2", dw2, _BF16, (H, I), d), b.stream_handle(stream)))

@@ -387,9 +387,11 @@ struct Operand {
     }
   }
 
+  // f(k): as many bits as the number of units is a multiple of, so that u ^ f(k) stays in the row, and
+  // different for the k whose rows start on the same banks
   static __device__ __forceinline__ int swz(int k) {
-    if constexpr (ROWS >= 128) return (k & 3) | ((k >> 1) & 4);
-    if constexpr (ROWS == 64) return ((k >> 1) & 1) | ((k >> 2) & 2);
+    if constexpr (ROWS % 128 == 0) return (k & 3) | ((k >> 1) & 4);
+    if constexpr (ROWS % 64 == 0) return ((k >> 1) & 1) | ((k >> 2) & 2);
     return (k >> 3) & 1;
   }
 
@@ -399,13 +401,14 @@ struct Operand {
     for (int i = 0; i < kPer; ++i)
       if (kMin == kPer || wave < kInstr) copy_to_lds(lds + (wave + i * NW) * 1024, base, off[i]);
   }
-  // The same where only the first `valid` bytes (k rows) of the step exist.
+  // The same where only the first `valid` bytes (k rows) of the step exist: the other lanes copy zeros.
   __device__ __forceinline__ void copy_tail(uint32_t lds, int wave, const char* base, int valid) const {
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (kMin == kPer || wave < kInstr)
-        copy_to_lds(lds + (wave + i * NW) * 1024,
-                    kc[i] < valid ? base + off[i] : reinterpret_cast<const char*>(g_zeros));
+      if (kMin == kPer || wave < kInstr) {
+        if (kc[i] < valid) copy_to_lds(lds + (wave + i * NW) * 1024, base, off[i]);
+        else copy_to_lds(lds + (wave + i * NW) * 1024, reinterpret_cast<const char*>(g_zeros), 0u);
+      }
   }
 };
 
@@ -570,6 +573,27 @@ __device__ __forceinline__ void finish_dglu(const DenseArgs& a, int64_t t, int n
   if (a.y) store_bf16(static_cast<uint16_t*>(a.y) + t * a.ldy + n, true, C, h);
 }
 
+// Columns n .. n + 7 of row t, whose accumulators are columns c .. c + 7 of the
+// fp32 row at `row` (a GLU's gate and up blocks of 16 alternate there).
+template <DenseOp OP>
+__device__ __forceinline__ void finish_chunk(const DenseArgs& a, int64_t t, int n, const float* row, int c) {
+  const bool in = t < a.T && n < a.N;
+  const float* p = row + (OP == DENSE_GLU ? (c >> 4) * 32 + (c & 15) : c);
+  float v[8];
+  *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(p);
+  *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(p + 4);
+  if constexpr (OP == DENSE_GLU) {
+    float u[8];
+    *reinterpret_cast<float4*>(u) = *reinterpret_cast<const float4*>(p + 16);
+    *reinterpret_cast<float4*>(u + 4) = *reinterpret_cast<const float4*>(p + 20);
+    finish_glu(a, t, n, in, v, u);
+  } else if constexpr (OP == DENSE_DGLU) {
+    if (in) finish_dglu(a, t, n, v);
+  } else {
+    if (in) finish_linear(a, t, n, v);
+  }
+}
+
 // Workgroups go round-robin over the 8 XCDs, each with its own L2.  Every XCD
 // takes a contiguous run of tiles, in bands of kBand tiles of t, column by
 // column, so that the tiles in flight together share rows of both operands.
@@ -642,7 +666,7 @@ __global__ __launch_bounds__(WT * WN * 64) void dense_tile_kernel(DenseArgs a) {
 
   auto fetch = [&](int k) {      // copies of step k
     const uint32_t st = lds0 + (k % NST) * kStage;
-    if (k < nk - 1 || tail == kstep) {
+    if (FP8 || k < nk - 1 || tail == kstep) {
       oa.copy(st, wave, pa + k * sa);
       ob.copy(st + kA, wave, pb + k * sb);
     } else {
@@ -753,22 +777,127 @@ __global__ __launch_bounds__(WT * WN * 64) void dense_tile_kernel(DenseArgs a) {
 #pragma unroll 1
   for (int idx = threadIdx.x; idx < BT * kChunks; idx += NW * 64) {
     const int r = idx / kChunks, c = (idx % kChunks) * 8;
-    const int64_t t = t0 + r;
-    const int n = n0 + c;
-    const bool in = t < a.T && n < a.N;
-    const float* p = tile + r * LR + (OP == DENSE_GLU ? (c >> 4) * 32 + (c & 15) : c);
-    float v[8];
-    *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(p);
-    *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(p + 4);
-    if constexpr (OP == DENSE_GLU) {
-      float u[8];
-      *reinterpret_cast<float4*>(u) = *reinterpret_cast<const float4*>(p + 16);
-      *reinterpret_cast<float4*>(u + 4) = *reinterpret_cast<const float4*>(p + 20);
-      finish_glu(a, t, n, in, v, u);
-    } else if constexpr (OP == DENSE_DGLU) {
-      if (in) finish_dglu(a, t, n, v);
-    } else {
-      if (in) finish_linear(a, t, n, v);
+    finish_chunk<OP>(a, t0 + r, n0 + c, tile + r * LR, c);
+  }
+}
+
+// The large bf16 tile: 256 rows of A by 32 FN (192 or 256) of B, eight wavefronts as
+// 4 x 2.  What bounds the 128 x 128 tile is the LDS port (fragment reads at 128 bytes a
+// clock plus the copies' writes at 60): 1058 clocks a step for 515 of MFMA.  A larger
+// tile moves fewer bytes per MFMA, but one workgroup then fills the unit and nothing
+// runs while its wavefronts read.  So they work in two groups of four (one wavefront
+// per SIMD each) half a step apart: while one group reads its fragments of 32 k and
+// issues copies, the other one's MFMAs run, and a barrier ends each phase.  A's step
+// is copied two steps ahead (three slots), B's one step ahead (two).
+template <DenseOp OP, bool AK, bool BK, int FN>
+__global__ __launch_bounds__(512) void dense_pair_kernel(DenseArgs a) {
+  constexpr int FT = 4, WN = 2, NW = 8, BT = 256, BN = WN * FN * 16;
+  constexpr int NO = OP == DENSE_GLU ? BN / 2 : BN;
+  constexpr int kA = BT * 128, kB = BN * 128;
+  extern __shared__ __align__(16) char lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wt = wave / WN, wn = wave % WN, group = wave / 4;
+  const int q4 = (lane >> 4) * 4, ln = lane & 15;
+  int tt, tn;
+  tile_of((a.T + BT - 1) / BT, (a.N + NO - 1) / NO, tt, tn);
+  const int t0 = tt * BT, n0 = tn * NO;
+  const int64_t lda = a.lda * 2, ldb = a.ldb * 2;
+
+  Operand<BT, NW, AK> oa;
+  Operand<BN, NW, BK> ob;
+  const char* pa = static_cast<const char*>(a.a) + (AK ? t0 * lda : 0);
+  const char* pb = static_cast<const char*>(a.b) + (BK ? n0 * ldb : 0);
+  oa.init(wave, lane, lda, [&](int r) { return (int64_t)min(r, a.T - 1 - t0); }, t0, a.T);
+  ob.init(wave, lane, ldb, [&](int r) {
+    if constexpr (OP == DENSE_GLU) return (int64_t)min((r >> 5) * 16 + (r & 15), a.N - 1 - n0);
+    return (int64_t)min(r, a.N - 1 - n0);
+  }, n0, a.N);
+  if (OP == DENSE_GLU && (wave & 2)) pb += (int64_t)a.N * ldb;
+  Frags<BT, AK, FT> fa;
+  Frags<BN, BK, FN> fb;
+  fa.init(wt * FT * 16, lane);
+  fb.init(wn * FN * 16, lane);
+  const int64_t sa = AK ? 128 : 64 * lda, sb = BK ? 128 : 64 * ldb;
+  const int nk = (a.K + 63) / 64;
+  const int tail = a.K - (nk - 1) * 64;
+  const uint32_t lds0 = lds_addr(lds);
+  auto copy_a = [&](int k) {
+    const uint32_t st = lds0 + k % 3 * kA;
+    if (k < nk - 1 || tail == 64) oa.copy(st, wave, pa + k * sa);
+    else oa.copy_tail(st, wave, pa + k * sa, AK ? tail * 2 : tail);
+  };
+  auto copy_b = [&](int k) {
+    const uint32_t st = lds0 + 3 * kA + k % 2 * kB;
+    if (k < nk - 1 || tail == 64) ob.copy(st, wave, pb + k * sb);
+    else ob.copy_tail(st, wave, pb + k * sb, BK ? tail * 2 : tail);
+  };
+  f32x4_t acc[FT][FN];
+#pragma unroll
+  for (int i = 0; i < FT; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  bf16x8_t af[FT], bf[FN];
+  auto read = [&](int k, int s) {
+    const char* la = lds + k % 3 * kA;
+    const char* lb = lds + 3 * kA + k % 2 * kB;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) bf[j] = fb.bf16(lb, j, s);
+#pragma unroll
+    for (int i = 0; i < FT; ++i) af[i] = fa.bf16(la, i, s);
+  };
+  auto multiply = [&] {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int i = 0; i < FT; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j], af[i], acc[i][j], 0, 0, 0);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_barrier" ::: "memory");
+  };
+  // everything has arrived but, with `newer`, the copies of A issued last
+  auto wait_all_but_a = [&](bool newer) {
+    if (newer) wait_stage<decltype(oa)::kPer>();
+    else wait_stage<0>();
+  };
+  if (nk > 0) {
+    copy_b(0);
+    copy_a(0);
+  }
+  if (nk > 1) copy_a(1);
+  wait_all_but_a(nk > 1);
+  if (group == 1) asm volatile("s_barrier" ::: "memory");
+  for (int k = 0; k < nk; ++k) {
+    read(k, 0);
+    if (k + 1 < nk) copy_b(k + 1);          // into the slot of step k - 1, which both groups have read
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    multiply();
+    read(k, 1);
+    if (k + 2 < nk) copy_a(k + 2);          // likewise
+    wait_all_but_a(k + 2 < nk);             // step k + 1 is there before the first group reads it, two phases on
+    multiply();
+  }
+  if (group == 0) asm volatile("s_barrier" ::: "memory");
+
+  // As in the smaller tile, half of each wavefront's blocks of rows at a time.
+  constexpr int LR = BN + 4, kChunks = NO / 8;
+  float* tile = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        *reinterpret_cast<f32x4_t*>(tile + (wt * 32 + i * 16 + ln) * LR + (wn * FN + j) * 16 + q4) = acc[2 * half + i][j];
+    __syncthreads();
+    static_assert(128 * kChunks % 64 == 0, "whole wavefronts finish chunks: scale groups stay together");
+#pragma unroll 1
+    for (int idx = threadIdx.x; idx < 128 * kChunks; idx += 512) {
+      const int r = idx / kChunks, c = (idx % kChunks) * 8;
+      finish_chunk<OP>(a, t0 + (r >> 5) * 64 + half * 32 + (r & 31), n0 + c, tile + r * LR, c);
     }
   }
 }
@@ -901,6 +1030,15 @@ void launch_tile(const DenseArgs& a, hipStream_t s) {
 
 }  // namespace
 
+template <DenseOp OP, bool AK, bool BK, int FN>
+static void launch_pair(const DenseArgs& a, hipStream_t s) {
+  constexpr int BN = 32 * FN, NO = OP == DENSE_GLU ? BN / 2 : BN;
+  constexpr size_t kLds = 3 * 256 * 128 + 2 * BN * 128;
+  static_assert(kLds <= 160 * 1024 && 128 * (BN + 4) * 4 <= kLds, "LDS of one workgroup");
+  const int64_t tiles = (int64_t)((a.T + 255) / 256) * ((a.N + NO - 1) / NO);
+  dense_pair_kernel<OP, AK, BK, FN><<<dim3((unsigned)tiles), 512, kLds, s>>>(a);
+}
+
 template <DenseOp OP, int FP8, int RW, int KW, int P, int U>
 static void launch_few_n(const DenseArgs& a, hipStream_t s) {
   constexpr int NR = 16 / P, NO = NR * RW / (OP == DENSE_GLU ? 2 : 1);
@@ -937,6 +1075,22 @@ static void launch_sized(const DenseArgs& a, hipStream_t s) {
     }
   }
   if (tiles(128, 128) >= 256) {
+    // Rounds of tiles over the 256 units (two 128 x 128 ones on each), in the time of a 256 x 256 tile:
+    // 256 x 192 takes 0.74 and two 128 x 128 0.64 of it (4096^3: 96, 2 x 71 and 2 x 61 us).  Not for the
+    // gradient of h: there the epilogue's bytes weigh as much, and smaller tiles overlap them.
+    if constexpr (FP8 == 0 && OP != DENSE_DGLU) {
+      auto rounds = [](int64_t n, int64_t per) { return (float)((n + per - 1) / per); };
+      const float big = rounds(tiles(256, 256), 256), mid = 0.74f * rounds(tiles(256, 192), 256);
+      const float small = 0.64f * rounds(tiles(128, 128), 512);
+      if (big < mid && big < small) {
+        launch_pair<OP, AK, BK, 8>(a, s);
+        return;
+      }
+      if (mid < small) {
+        launch_pair<OP, AK, BK, 6>(a, s);
+        return;
+      }
+    }
     if constexpr (FP8 != 0) launch_tile<OP, FP8, AK, BK, 4, 2, 2, 4, 2>(a, s);
     else if constexpr (OP == DENSE_DGLU) launch_tile<OP, FP8, AK, BK, 2, 4, 4, 2, 2>(a, s);
     else launch_tile<OP, FP8, AK, BK, 2, 2, 4, 4, 2>(a, s);

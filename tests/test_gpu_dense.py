@@ -254,6 +254,63 @@ def test_linear(T, N, K, fp8):
         ok()
 
 
+@pytest.mark.parametrize("T,N,K", [(4096, 4096, 64), (4096, 4096, 136), (4095, 4099, 200), (2050, 12290, 72),
+                                   (8192, 2048, 512), (1000, 9000, 64), (2048, 6144, 128)])
+def test_linear_of_many_rows(T, N, K):
+    """Enough output for the larger tiles: a sample of rows and columns, the edges among them, against the oracle."""
+    rng = np.random.default_rng(T + N)
+    x, xv = _bf(rng.standard_normal((T, K)))
+    w, wv = _bf(rng.standard_normal((N, K)) * 0.1)
+    bias, bv = _bf(rng.standard_normal(N))
+    out, ok = _padded(T, N)
+    pe.linear(x, w, out, bias=bias)
+    torch.cuda.synchronize()
+    ok()
+    rows = np.unique(np.concatenate([[0, T - 1, 255 % T, 256 % T], rng.integers(0, T, 60)]))
+    y = xv[rows] @ wv.T + bv
+    err = (K + 8) * 2.0 ** -24 * (np.abs(xv[rows]) @ np.abs(wv).T + np.abs(y) + np.abs(bv))
+    _within(_np(out)[rows], y, err + BF * (np.abs(y) + err))
+
+
+@pytest.mark.parametrize("T,H,I", [(2048, 64, 6144), (2000, 136, 6152), (4096, 72, 2048), (4096, 64, 3000)])
+def test_glu_of_many_rows(T, H, I):
+    rng = np.random.default_rng(T + I)
+    x, xv = _bf(rng.standard_normal((T, H)))
+    w, wv = _bf(rng.standard_normal((2 * I, H)) * 0.1)
+    out, ok = _padded(T, I)
+    gu = torch.empty((T, 2 * I), dtype=torch.bfloat16, device=DEV)
+    pe.glu(x, w, out, gu=gu)
+    torch.cuda.synchronize()
+    ok()
+    rows = np.unique(np.concatenate([[0, T - 1], rng.integers(0, T, 30)]))
+    g, u, h = dense.glu(xv[rows], wv, "silu")
+    mag = np.abs(xv[rows]) @ np.abs(wv).T * (H + 8) * 2.0 ** -24
+    ag = np.abs(dense.act(g, "silu"))
+    err = (1.13 * mag[:, :I] + FN * ag) * (np.abs(u) + mag[:, I:]) + ag * mag[:, I:] + 2.0 ** -23 * np.abs(h)
+    _within(_np(out)[rows], h, err + BF * (np.abs(h) + err), "h")
+    both = np.concatenate([g, u], 1)
+    _within(_np(gu)[rows], both, mag + BF * (np.abs(both) + mag), "gu")
+
+
+def test_ffn_backward_of_wide_weights():
+    """Weight gradients large enough for the larger tiles over k-slow operands, with a ragged number of tokens."""
+    T, H, I = 70, 2048, 6144
+    dev, val = _backward_case(T, H, I, "silu", 17)
+    x, w13, w2, dy, gu = dev
+    xv, w13v, w2v, dyv, guv = val
+    bufs = [torch.empty(s, dtype=torch.bfloat16, device=DEV) for s in ((T, 2 * I), (T, I), (2 * I, H), (H, I))]
+    pe.ffn_backward(dy, x, gu, w13, w2, bufs[0], bufs[1], dw13=bufs[2], dw2=bufs[3])
+    torch.cuda.synchronize()
+    dguv, hv = _np(bufs[0]), _np(bufs[1])              # the products' own inputs
+    for got, left, right in ((bufs[2], dguv, xv), (bufs[3], dyv, hv)):
+        ref = left.T @ right
+        err = (T + 8) * 2.0 ** -24 * (np.abs(left).T @ np.abs(right))
+        _within(_np(got), ref, err + BF * (np.abs(ref) + err) + 1e-30)
+    g, u = guv[:, :I], guv[:, I:]
+    h = dense.act(g, "silu") * u
+    _within(hv, h, np.abs(h) * (BF + 2 * FN), "h")
+
+
 def test_linear_into_its_residual():
     rng = np.random.default_rng(5)
     for T, N, K, fp8 in [(3, 100, 256, False), (200, 300, 256, False), (130, 256, 384, True)]:

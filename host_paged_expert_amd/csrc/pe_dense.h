@@ -68,5 +68,7 @@ void launch_rmsnorm(const NormArgs& a, hipStream_t s);
 void launch_route(const RouteArgs& a, hipStream_t s);
 // fp8: both operands are e4m3 with scales; ak / bk: the operand is K-major.
 void launch_dense(DenseOp op, bool fp8, bool ak, bool bk, const DenseArgs& a, hipStream_t s);
+// The products dx (A K-major, B k-slow), dw13 and dw2 (both k-slow); any may be null.
+void launch_dense_grads(const DenseArgs* dx, const DenseArgs* dw13, const DenseArgs* dw2, hipStream_t s);
 
 }  // namespace pe

@@ -597,9 +597,9 @@ __device__ __forceinline__ void finish_chunk(const DenseArgs& a, int64_t t, int 
 // Workgroups go round-robin over the 8 XCDs, each with its own L2.  Every XCD
 // takes a contiguous run of tiles, in bands of kBand tiles of t, column by
 // column, so that the tiles in flight together share rows of both operands.
-__device__ __forceinline__ void tile_of(int nt, int nn, int& tt, int& tn) {
+__device__ __forceinline__ void tile_of(int b, int nt, int nn, int& tt, int& tn) {
   constexpr int kXcds = 8, kBand = 8;
-  const int total = nt * nn, b = blockIdx.x;
+  const int total = nt * nn;
   const int xcd = b % kXcds, per = total / kXcds, rem = total % kXcds;
   const int q = xcd * per + min(xcd, rem) + b / kXcds;
   const int band = q / (kBand * nn), rows = min(kBand, nt - band * kBand), r = q - band * kBand * nn;
@@ -620,7 +620,7 @@ constexpr int tile_lds(int bt, int bn, int nst, int fp8) {
 // A GLU tile's B rows alternate 16 gate rows and the 16 up rows of the same
 // columns, so that a wavefront holds both products of its columns.
 template <DenseOp OP, int FP8, bool AK, bool BK, int WT, int WN, int FT, int FN, int NST>
-__global__ __launch_bounds__(WT * WN * 64) void dense_tile_kernel(DenseArgs a) {
+__device__ __forceinline__ void dense_tile(const DenseArgs& a, int block) {
   constexpr int NW = WT * WN, BT = WT * FT * 16, BN = WN * FN * 16;
   constexpr int NO = OP == DENSE_GLU ? BN / 2 : BN;       // output columns per tile
   constexpr int ES = FP8 ? 1 : 2;
@@ -630,7 +630,7 @@ __global__ __launch_bounds__(WT * WN * 64) void dense_tile_kernel(DenseArgs a) {
   const int wt = wave / WN, wn = wave % WN;
   const int q4 = (lane >> 4) * 4, ln = lane & 15;
   int tt, tn;
-  tile_of((a.T + BT - 1) / BT, (a.N + NO - 1) / NO, tt, tn);
+  tile_of(block, (a.T + BT - 1) / BT, (a.N + NO - 1) / NO, tt, tn);
   const int t0 = tt * BT, n0 = tn * NO;
   const int64_t lda = a.lda * ES, ldb = a.ldb * ES;
 
@@ -781,6 +781,21 @@ __global__ __launch_bounds__(WT * WN * 64) void dense_tile_kernel(DenseArgs a) {
   }
 }
 
+template <DenseOp OP, int FP8, bool AK, bool BK, int WT, int WN, int FT, int FN, int NST>
+__global__ __launch_bounds__(WT * WN * 64) void dense_tile_kernel(DenseArgs a) {
+  dense_tile<OP, FP8, AK, BK, WT, WN, FT, FN, NST>(a, blockIdx.x);
+}
+
+// The three products of the feed-forward gradients in one launch of 64 x 64 tiles: dx's
+// (the longest sums) first, then dw13's and dw2's.
+__global__ __launch_bounds__(256) void dense_grads_kernel(DenseArgs dx, DenseArgs dw13, DenseArgs dw2, int n_dx,
+                                                          int n_dw13) {
+  const int b = blockIdx.x;
+  if (b < n_dx) dense_tile<DENSE_LINEAR, 0, true, false, 2, 2, 2, 2, 2>(dx, b);
+  else if (b < n_dx + n_dw13) dense_tile<DENSE_LINEAR, 0, false, false, 2, 2, 2, 2, 2>(dw13, b - n_dx);
+  else dense_tile<DENSE_LINEAR, 0, false, false, 2, 2, 2, 2, 2>(dw2, b - n_dx - n_dw13);
+}
+
 // The large bf16 tile: 256 rows of A by 32 FN (192 or 256) of B, eight wavefronts as
 // 4 x 2.  What bounds the 128 x 128 tile is the LDS port (fragment reads at 128 bytes a
 // clock plus the copies' writes at 60): 1058 clocks a step for 515 of MFMA.  A larger
@@ -799,7 +814,7 @@ __global__ __launch_bounds__(512) void dense_pair_kernel(DenseArgs a) {
   const int wt = wave / WN, wn = wave % WN, group = wave / 4;
   const int q4 = (lane >> 4) * 4, ln = lane & 15;
   int tt, tn;
-  tile_of((a.T + BT - 1) / BT, (a.N + NO - 1) / NO, tt, tn);
+  tile_of(blockIdx.x, (a.T + BT - 1) / BT, (a.N + NO - 1) / NO, tt, tn);
   const int t0 = tt * BT, n0 = tn * NO;
   const int64_t lda = a.lda * 2, ldb = a.ldb * 2;
 
@@ -1091,8 +1106,11 @@ static void launch_sized(const DenseArgs& a, hipStream_t s) {
         return;
       }
     }
-    if constexpr (FP8 != 0) launch_tile<OP, FP8, AK, BK, 4, 2, 2, 4, 2>(a, s);
-    else if constexpr (OP == DENSE_DGLU) launch_tile<OP, FP8, AK, BK, 2, 4, 4, 2, 2>(a, s);
+    if constexpr (FP8 != 0) {
+      // one 128 x 128 tile a unit leaves it waiting for its copies: two of 64 x 128 (2048 x 2048 x 6144: 57 -> 50 us)
+      if (tiles(128, 128) <= 256) launch_tile<OP, FP8, AK, BK, 2, 2, 2, 4, 2>(a, s);
+      else launch_tile<OP, FP8, AK, BK, 4, 2, 2, 4, 2>(a, s);
+    } else if constexpr (OP == DENSE_DGLU) launch_tile<OP, FP8, AK, BK, 2, 4, 4, 2, 2>(a, s);
     else launch_tile<OP, FP8, AK, BK, 2, 2, 4, 4, 2>(a, s);
   } else if (tiles(64, 64) > 256) {
     launch_tile<OP, FP8, AK, BK, 2, 2, 2, 2, 2>(a, s);
@@ -1114,6 +1132,22 @@ void launch_dense(DenseOp op, bool fp8, bool ak, bool bk, const DenseArgs& a, hi
   else if (ak && bk) launch_sized<DENSE_LINEAR, 0, true, true>(a, s);
   else if (ak) launch_sized<DENSE_LINEAR, 0, true, false>(a, s);
   else launch_sized<DENSE_LINEAR, 0, false, false>(a, s);
+}
+
+void launch_dense_grads(const DenseArgs* dx, const DenseArgs* dw13, const DenseArgs* dw2, hipStream_t s) {
+  auto tiles = [](const DenseArgs& a, int side) {
+    return (int64_t)((a.T + side - 1) / side) * ((a.N + side - 1) / side);
+  };
+  // Where none fills the units with larger tiles, one launch (257 x 2048 x 768: 22 us of launches one after
+  // another become 13); larger ones go by themselves, each with the tile it is best with.
+  if (dx && dw13 && dw2 && dx->K > 0 && tiles(*dx, 128) < 256 && tiles(*dw13, 128) < 256 && tiles(*dw2, 128) < 256) {
+    const int n0 = (int)tiles(*dx, 64), n1 = (int)tiles(*dw13, 64), n2 = (int)tiles(*dw2, 64);
+    dense_grads_kernel<<<dim3(n0 + n1 + n2), 256, tile_lds(64, 64, 2, 0), s>>>(*dx, *dw13, *dw2, n0, n1);
+    return;
+  }
+  if (dx) launch_dense(DENSE_LINEAR, false, true, false, *dx, s);
+  if (dw13) launch_dense(DENSE_LINEAR, false, false, false, *dw13, s);
+  if (dw2) launch_dense(DENSE_LINEAR, false, false, false, *dw2, s);
 }
 
 }  // namespace pe

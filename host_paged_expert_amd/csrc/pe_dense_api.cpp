@@ -310,33 +310,23 @@ int pe_ffn_backward(int device, int act, const void* dy, int64_t lddy, const voi
     pe::launch_dense(pe::DENSE_DGLU, false, true, false, a, s);
     PE_HIP(hipGetLastError());
   }
-  pe::DenseArgs p{};
-  p.act = PE_ACT_NONE;
-  p.vec = 1;
-  if (T > 0 && dx) {
-    p.a = dgu; p.lda = 2 * I;
-    p.b = w13; p.ldb = H;
-    p.T = T; p.N = H; p.K = 2 * I;
-    p.y = dx; p.ldy = lddx;
-    pe::launch_dense(pe::DENSE_LINEAR, false, true, false, p, s);
-    PE_HIP(hipGetLastError());
-  }
-  if (dw13) {   // with T = 0 a sum of nothing: zeros
-    p.a = dgu; p.lda = 2 * I;
-    p.b = x; p.ldb = ldx;
-    p.T = 2 * I; p.N = H; p.K = T;
-    p.y = dw13; p.ldy = H;
-    pe::launch_dense(pe::DENSE_LINEAR, false, false, false, p, s);
-    PE_HIP(hipGetLastError());
-  }
-  if (dw2) {
-    p.a = dy; p.lda = lddy;
-    p.b = h; p.ldb = I;
-    p.T = H; p.N = I; p.K = T;
-    p.y = dw2; p.ldy = I;
-    pe::launch_dense(pe::DENSE_LINEAR, false, false, false, p, s);
-    PE_HIP(hipGetLastError());
-  }
+  auto product = [&](const void* left, int64_t ld_l, const void* right, int64_t ld_r, int rows, int cols, int sum,
+                     void* out, int64_t ld_o) {
+    pe::DenseArgs p{};
+    p.act = PE_ACT_NONE;
+    p.vec = 1;
+    p.a = left; p.lda = ld_l;
+    p.b = right; p.ldb = ld_r;
+    p.T = rows; p.N = cols; p.K = sum;
+    p.y = out; p.ldy = ld_o;
+    return p;
+  };
+  // with T = 0 the weight gradients are sums of nothing: zeros
+  const pe::DenseArgs gx = product(dgu, 2 * (int64_t)I, w13, H, T, H, 2 * I, dx, lddx);
+  const pe::DenseArgs g13 = product(dgu, 2 * (int64_t)I, x, ldx, 2 * I, H, T, dw13, H);
+  const pe::DenseArgs g2 = product(dy, lddy, h, I, H, I, T, dw2, I);
+  pe::launch_dense_grads(T > 0 && dx ? &gx : nullptr, dw13 ? &g13 : nullptr, dw2 ? &g2 : nullptr, s);
+  PE_HIP(hipGetLastError());
   return PE_OK;
 }
 

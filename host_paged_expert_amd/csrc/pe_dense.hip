@@ -144,20 +144,37 @@ __global__ __launch_bounds__(256) void rmsnorm_kernel(NormArgs a) {
       ss = __builtin_fmaf(v[i][e], v[i][e], ss);
     }
   }
-  ss = group_sum<64>(ss);
-  if constexpr (WPR == 4) {
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = ss;
-    __syncthreads();
-    ss = (part[0] + part[1]) + (part[2] + part[3]);
+  auto over_row = [&](float s) {
+    s = group_sum<64>(s);
+    if constexpr (WPR == 4) {
+      __syncthreads();
+      if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+      __syncthreads();
+      s = (part[0] + part[1]) + (part[2] + part[3]);
+    }
+    return s;
+  };
+  ss = over_row(ss);
+  float pre = 1.f, eps = a.eps;
+  if (ss == __builtin_inff()) {          // (the same in all of a row's lanes)
+    // Squares past fp32's range: sum those of 2^-70 v, beside which eps is nothing.
+    pre = 0x1p-70f;
+    eps = 0.f;
+    ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[i][e] * pre, v[i][e] * pre, ss);
+    ss = over_row(ss);
   }
-  const float inv = 1.f / sqrtf(ss / (float)a.H + a.eps);
+  const float inv = 1.f / sqrtf(ss / (float)a.H + eps);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = l + i * kLanes;
     float wv[8], y[8];
     widen8(wc[i], wv);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = v[i][e] * inv * wv[e];
+    for (int e = 0; e < 8; ++e) y[e] = v[i][e] * pre * inv * wv[e];
     if (a.sum && c < n_ch) reinterpret_cast<uint4*>(a.sum + t * a.lds)[c] = narrow8(v[i]);
     if (!a.yscale) {
       if (c < n_ch) reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + t * a.ldy)[c] = narrow8(y);
@@ -727,20 +744,25 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int block) {
 #pragma unroll
           for (int s = 0; s < 4; ++s) aw[s] = widen_e4m3(af[2 * s], af[2 * s + 1]);
         }
+        f32x4_t p[FN];
+        if constexpr (FP8 == 2) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          f32x4_t p = f32x4_t{0.f, 0.f, 0.f, 0.f};
-          if constexpr (FP8 == 2) {
+          for (int s = 0; s < 4; ++s)
 #pragma unroll
-            for (int s = 0; s < 4; ++s) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bw[j][s], aw[s], p, 0, 0, 0);
-          } else {
-            p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                bf[j], af, p, 0, 0, 0, 0, 0, 0);   // no block scales
-          }
-          const float s = OP == DENSE_GLU && (j & 1) ? s1 : s0;
+            for (int j = 0; j < FN; ++j)
+              p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bw[j][s], aw[s],
+                                                             s ? p[j] : f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+        } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[e], s, acc[i][j][e]);
+          for (int j = 0; j < FN; ++j)
+            p[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0,
+                                                                    0);   // no block scales
         }
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[i][j][e] = __builtin_fmaf(p[j][e], OP == DENSE_GLU && (j & 1) ? s1 : s0, acc[i][j][e]);
       }
     } else {
 #pragma unroll
@@ -796,7 +818,7 @@ __global__ __launch_bounds__(256) void dense_grads_kernel(DenseArgs dx, DenseArg
   else dense_tile<DENSE_LINEAR, 0, false, false, 2, 2, 2, 2, 2>(dw2, b - n_dx - n_dw13);
 }
 
-// The large bf16 tile: 256 rows of A by 32 FN (192 or 256) of B, eight wavefronts as
+// The large bf16 tile: 256 rows of A by 32 FN (128, 192 or 256) of B, eight wavefronts as
 // 4 x 2.  What bounds the 128 x 128 tile is the LDS port (fragment reads at 128 bytes a
 // clock plus the copies' writes at 60): 1058 clocks a step for 515 of MFMA.  A larger
 // tile moves fewer bytes per MFMA, but one workgroup then fills the unit and nothing
@@ -1070,7 +1092,7 @@ static void launch_sized(const DenseArgs& a, hipStream_t s) {
       if (tiles(16, 256) <= 256) launch_tile<OP, FP8, AK, BK, 1, 8, 1, 2, 4>(a, s);
       else if (tiles(32, 256) <= 256) launch_tile<OP, FP8, AK, BK, 1, 8, 2, 2, 4>(a, s);
       else if (tiles(64, 256) <= 256) launch_tile<OP, FP8, AK, BK, 1, 8, 4, 2, 3>(a, s);
-      else launch_tile<OP, FP8, AK, BK, 2, 4, 4, 4, 2>(a, s);
+      else launch_tile<OP, FP8, AK, BK, 2, 4, 4, 4, 3>(a, s);
       return;
     }
   }
@@ -1090,28 +1112,30 @@ static void launch_sized(const DenseArgs& a, hipStream_t s) {
     }
   }
   if (tiles(128, 128) >= 256) {
-    // Rounds of tiles over the 256 units (two 128 x 128 ones on each), in the time of a 256 x 256 tile:
-    // 256 x 192 takes 0.74 and two 128 x 128 0.64 of it (4096^3: 96, 2 x 71 and 2 x 61 us).  Not for the
-    // gradient of h: there the epilogue's bytes weigh as much, and smaller tiles overlap them.
+    // The fewest rounds of tiles over the 256 units, each in the time of a 256 x 256 tile's (us for one round of
+    // 4096 k: 99 with K-major operands, 98 with both k-slow): 256 x 192 takes 0.75 (0.86), 256 x 128 0.62 (0.72),
+    // and two 128 x 128 a unit 0.68 (0.62).  Not for the gradient of h: there the epilogue's bytes weigh as much,
+    // and the smaller tiles of two workgroups a unit overlap them (4096 x 6144 x 2048: 144 against 164 us).
     if constexpr (FP8 == 0 && OP != DENSE_DGLU) {
       auto rounds = [](int64_t n, int64_t per) { return (float)((n + per - 1) / per); };
-      const float big = rounds(tiles(256, 256), 256), mid = 0.74f * rounds(tiles(256, 192), 256);
-      const float small = 0.64f * rounds(tiles(128, 128), 512);
-      if (big < mid && big < small) {
-        launch_pair<OP, AK, BK, 8>(a, s);
-        return;
-      }
-      if (mid < small) {
-        launch_pair<OP, AK, BK, 6>(a, s);
-        return;
-      }
+      constexpr bool slow = !AK && !BK;
+      const float c256 = rounds(tiles(256, 256), 256), c192 = (slow ? 0.86f : 0.75f) * rounds(tiles(256, 192), 256);
+      const float c128 = (slow ? 0.72f : 0.62f) * rounds(tiles(256, 128), 256);
+      const float small = (slow ? 0.62f : 0.68f) * rounds(tiles(128, 128), 512);
+      const float best = std::min(std::min(c256, c192), std::min(c128, small));
+      if (best == c256) launch_pair<OP, AK, BK, 8>(a, s);
+      else if (best == c192) launch_pair<OP, AK, BK, 6>(a, s);
+      else if (best == c128) launch_pair<OP, AK, BK, 4>(a, s);
+      else launch_tile<OP, FP8, AK, BK, 2, 2, 4, 4, 2>(a, s);
+      return;
     }
     if constexpr (FP8 != 0) {
       // one 128 x 128 tile a unit leaves it waiting for its copies: two of 64 x 128 (2048 x 2048 x 6144: 57 -> 50 us)
       if (tiles(128, 128) <= 256) launch_tile<OP, FP8, AK, BK, 2, 2, 2, 4, 2>(a, s);
       else launch_tile<OP, FP8, AK, BK, 4, 2, 2, 4, 2>(a, s);
-    } else if constexpr (OP == DENSE_DGLU) launch_tile<OP, FP8, AK, BK, 2, 4, 4, 2, 2>(a, s);
-    else launch_tile<OP, FP8, AK, BK, 2, 2, 4, 4, 2>(a, s);
+    } else {
+      launch_tile<OP, FP8, AK, BK, 2, 4, 4, 2, 2>(a, s);
+    }
   } else if (tiles(64, 64) > 256) {
     launch_tile<OP, FP8, AK, BK, 2, 2, 2, 2, 2>(a, s);
   } else if (tiles(64, 64) > 128) {

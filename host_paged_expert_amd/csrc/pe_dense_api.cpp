@@ -69,9 +69,10 @@ struct DeviceScope {
   hipError_t err;
   explicit DeviceScope(int device) {
     err = hipGetDevice(&prev);
-    if (err != hipSuccess) { prev = -1; return; }
-    if (prev == device) prev = -1;
+    if (err != hipSuccess) prev = -1;
+    else if (prev == device) prev = -1;
     else err = hipSetDevice(device);
+    if (err != hipSuccess) (void)hipGetLastError();   // reported here; the next call's launch must not find it
   }
   ~DeviceScope() {
     if (prev >= 0) (void)hipSetDevice(prev);
@@ -84,8 +85,12 @@ struct DeviceScope {
     if (rc_ != PE_OK) return rc_; \
   } while (0)
 
-int check_dims(int device, std::initializer_list<int> dims) {
+// A launch has fewer than 2^32 threads: 256 for each of T rows at most.
+constexpr int kMaxRows = 1 << 24;
+
+int check_dims(int device, int T, std::initializer_list<int> dims) {
   if (device < 0) return fail(PE_ERR_INVALID_ARG, "device %d is negative", device);
+  if (T < 0 || T >= kMaxRows) return fail(PE_ERR_INVALID_ARG, "T=%d outside [0, 2^24)", T);
   for (int d : dims)
     if (d < 1) return fail(PE_ERR_INVALID_ARG, "dimensions must be positive");
   return PE_OK;
@@ -119,8 +124,7 @@ extern "C" {
 
 int pe_rmsnorm(int device, const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
                float eps, int T, int H, void* sum, int64_t lds, void* y, int64_t ldy, float* yscale, void* stream) {
-  PE_TRY(check_dims(device, {H}));
-  if (T < 0) return fail(PE_ERR_INVALID_ARG, "T=%d is negative", T);
+  PE_TRY(check_dims(device, T, {H}));
   if (!(eps >= 0.f)) return fail(PE_ERR_INVALID_ARG, "eps must not be negative");
   if (H > PE_MAX_NORM_HIDDEN) return fail(PE_ERR_INVALID_ARG, "H=%d is larger than %d", H, PE_MAX_NORM_HIDDEN);
   if (yscale ? H % 128 : H % 8)
@@ -154,8 +158,7 @@ int pe_rmsnorm(int device, const void* x, int64_t ldx, const void* residual, int
 int pe_route(int device, const float* logits, int64_t ldl, int T, int num_experts, int top_k, int scoring,
              int renormalize, float scale, int32_t* topk_ids, float* topk_w, void* stream) {
   const int E = num_experts, k = top_k;
-  PE_TRY(check_dims(device, {E, k}));
-  if (T < 0) return fail(PE_ERR_INVALID_ARG, "T=%d is negative", T);
+  PE_TRY(check_dims(device, T, {E, k}));
   if (E > pe::kMaxExperts || k > E) return fail(PE_ERR_INVALID_ARG, "need top_k <= num_experts <= %d", pe::kMaxExperts);
   if (scoring != PE_SCORE_SOFTMAX && scoring != PE_SCORE_SIGMOID)
     return fail(PE_ERR_INVALID_ARG, "unknown scoring %d", scoring);
@@ -182,8 +185,7 @@ int pe_route(int device, const float* logits, int64_t ldl, int T, int num_expert
 int pe_linear(int device, int wtype, const void* x, int64_t ldx, const float* xscale, const void* w,
               const float* wscale, const void* bias, int act, const void* residual, int64_t ldr, int T, int N,
               int K, void* y, int64_t ldy, int ytype, void* stream) {
-  PE_TRY(check_dims(device, {N, K}));
-  if (T < 0) return fail(PE_ERR_INVALID_ARG, "T=%d is negative", T);
+  PE_TRY(check_dims(device, T, {N, K}));
   PE_TRY(check_wtype(wtype, K));
   PE_TRY(check_act(act, true));
   if (ytype != PE_Y_BF16 && ytype != PE_Y_FP32) return fail(PE_ERR_INVALID_ARG, "unknown output type %d", ytype);
@@ -226,8 +228,7 @@ int pe_glu(int device, int wtype, int act, const void* x, int64_t ldx, const flo
            const float* s13, int T, int hidden, int inter, void* h, int64_t ldh, float* hscale, void* gu,
            void* stream) {
   const int H = hidden, I = inter;
-  PE_TRY(check_dims(device, {H, I}));
-  if (T < 0) return fail(PE_ERR_INVALID_ARG, "T=%d is negative", T);
+  PE_TRY(check_dims(device, T, {H, I}));
   PE_TRY(check_wtype(wtype, H));
   PE_TRY(check_act(act, false));
   const bool fp8 = wtype == PE_W_FP8_B128;
@@ -270,8 +271,7 @@ int pe_ffn_backward(int device, int act, const void* dy, int64_t lddy, const voi
                     const void* w13, const void* w2, int T, int hidden, int inter, void* dgu, void* h, void* dx,
                     int64_t lddx, void* dw13, void* dw2, void* stream) {
   const int H = hidden, I = inter;
-  PE_TRY(check_dims(device, {H, I}));
-  if (T < 0) return fail(PE_ERR_INVALID_ARG, "T=%d is negative", T);
+  PE_TRY(check_dims(device, T, {H, I}));
   PE_TRY(check_act(act, false));
   if (H % 8 || I % 8)
     return fail(PE_ERR_INVALID_ARG, "hidden and inter must be multiples of 8");

@@ -309,7 +309,7 @@ int pe_forward_static(pe_ctx* ctx, int layer, const void* x, const int32_t* topk
  * row-major; a row stride (ld*) counts elements, is at least the row's length
  * and, like every row's length, below 2^22.  Matrices without one are contiguous.  Where nothing else is
  * said, addresses and row strides are multiples of 16 bytes, outputs overlap
- * no input and no other output, and T = 0 is a no-op.  Rows are independent
+ * no input and no other output, T is below 2^24, and T = 0 is a no-op.  Rows are independent
  * of each other.  Sums are fp32. */
 
 /* activations */

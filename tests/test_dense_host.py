@@ -50,7 +50,9 @@ REFUSED = [
     (_norm, dict(y=A[0] + 512)), (_norm, dict(y=A[3])), (_norm, dict(y=A[0], ldy=512)), (_norm, dict(sum_out=A[2])),
     (_norm, dict(y=A[0], yscale=A[5])), (_norm, dict(yscale=A[4] + 4)), (_norm, dict(H=16384 + 128, ldx=32768, ldr=32768,
                                                                                  lds=32768, ldy=32768)),
-    (_norm, dict(ldx=2 ** 31)),
+    (_norm, dict(ldx=2 ** 31)), (_norm, dict(ldx=2 ** 22)), (_norm, dict(T=2 ** 24)), (_route, dict(T=2 ** 24)),
+    (_linear, dict(T=2 ** 24)), (_linear, dict(N=2 ** 22, ldr=2 ** 22, ldy=2 ** 22)), (_glu, dict(T=2 ** 24)),
+    (_back, dict(T=2 ** 24)),
     (_route, dict(logits=None)), (_route, dict(topk_ids=None)), (_route, dict(topk_w=None)), (_route, dict(top_k=65)),
     (_route, dict(top_k=0)), (_route, dict(num_experts=1025, ldl=1025)), (_route, dict(scoring=2)),
     (_route, dict(T=-1)), (_route, dict(ldl=63)), (_route, dict(topk_ids=A[0])), (_route, dict(topk_w=A[1] + 16)),

@@ -162,6 +162,25 @@ def test_rmsnorm_in_place_and_special_rows():
     _within(q[fine], y[fine], np.abs(y[fine]) * (F8 + 1e-4) + np.repeat(_np(sc), 128, 1)[fine] * 2.0 ** -9.9, "codes")
 
 
+@pytest.mark.parametrize("H", [256, 2048, 8192])
+def test_rmsnorm_of_large_values(H):
+    """Squares beyond fp32's range: the norm is still the formula's; ordinary rows beside them are not touched."""
+    rng = np.random.default_rng(H)
+    a = rng.standard_normal((5, H))
+    a[1] *= 1e30
+    a[3, 7] = 3e38
+    x, xv = _bf(a)
+    w, wv = _bf(1 + 0.1 * rng.standard_normal(H))
+    _, y = dense.rmsnorm(xv, None, wv, 1e-6)
+    out, ok = _padded(5, H)
+    pe.rmsnorm(x, w, 1e-6, out)
+    torch.cuda.synchronize()
+    # two more fp32 operations than ordinary rows; what the scaled squares lose is below 2^-126 of a sum of 2^70 or more,
+    # and an element of 1 beside 3e38 is a subnormal number times 2^70: an absolute error of 2^-80 at most
+    _within(_np(out), y, np.abs(y) * (BF + (H / 2 + 20) * 2.0 ** -24) + 2.0 ** -80, "y")
+    ok()
+
+
 # ------------------------------------------------------------------ routing
 
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (5, 7, 7), (4, 128, 8), (3, 64, 6), (9, 65, 3), (33, 32, 4),
@@ -461,6 +480,40 @@ def test_ffn_backward_of_no_tokens():
                     dw2=d2)
     torch.cuda.synchronize()
     assert bool((d13 == 0).all()) and bool((d2 == 0).all())
+
+
+def test_no_tokens_and_byte_codes():
+    """T = 0 through the tensor functions (weight gradients of larger tiles too), and e4m3 codes as bytes."""
+    H, I = 2048, 6144
+    e = lambda *s, dt=torch.bfloat16: torch.empty(s, dtype=dt, device=DEV)    # noqa: E731
+    pe.rmsnorm(e(0, H), e(H), 1e-6, e(0, H))
+    pe.route(e(0, 8, dt=torch.float32), e(0, 2, dt=torch.int32), e(0, 2, dt=torch.float32))
+    pe.linear(e(0, H), e(16, H), e(0, 16))
+    pe.glu(e(0, H), e(32, H), e(0, 16))
+    d13 = torch.full((2 * I, H), GUARD, dtype=torch.bfloat16, device=DEV)
+    d2 = torch.full((H, I), GUARD, dtype=torch.bfloat16, device=DEV)
+    pe.ffn_backward(e(0, H), e(0, H), e(0, 2 * I), e(2 * I, H), e(H, I), e(0, 2 * I), e(0, I), dw13=d13, dw2=d2)
+    torch.cuda.synchronize()
+    assert bool((d13 == 0).all()) and bool((d2 == 0).all())
+    rng = np.random.default_rng(0)
+    args, *_ = _linear_case(20, 48, 256, True, rng)
+    out = [e(20, 48) for _ in range(2)]
+    pe.linear(out=out[0], **args)
+    args["x"], args["w"] = args["x"].view(torch.uint8), args["w"].view(torch.uint8)
+    pe.linear(out=out[1], **args)
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], out[1])
+
+
+def test_a_refused_call_leaves_the_next_one_alone():
+    x = torch.ones((2, 64), dtype=torch.bfloat16, device=DEV)
+    w = torch.ones((16, 64), dtype=torch.bfloat16, device=DEV)
+    y = torch.zeros((2, 16), dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(pe.PEError):
+        pe.pe_linear(99, 0, x, 64, None, w, None, None, 0, None, 0, 2, 16, 64, y, 16, 0)     # no such device
+    pe.linear(x, w, y)
+    torch.cuda.synchronize()
+    assert bool((y == 64).all())
 
 
 def test_gradients_match_differences_of_the_forward():

@@ -345,12 +345,20 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 __device__ __forceinline__ void copy_to_lds(uint32_t lds, const char* base, uint32_t off) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base));
 }
+// Same from an address of each lane.
 __device__ __forceinline__ void copy_to_lds(uint32_t lds, const char* p) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p));
 }
 // Same for 4 bytes per lane to 256 bytes of LDS.
 __device__ __forceinline__ void copy_to_lds4(uint32_t lds, const char* p) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(p));
+}
+
+// A pointer that is the same in all lanes, which the compiler does not always see.
+__device__ __forceinline__ const char* uniform(const char* p) {
+  const uint64_t b = (uint64_t)p;
+  return (const char*)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(b >> 32)) << 32 |
+                       (uint32_t)__builtin_amdgcn_readfirstlane((int)b));
 }
 
 // This wavefront's copies are done but for the newest N, its LDS reads are
@@ -422,10 +430,9 @@ struct Operand {
   __device__ __forceinline__ void copy_tail(uint32_t lds, int wave, const char* base, int valid) const {
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (kMin == kPer || wave < kInstr) {
-        if (kc[i] < valid) copy_to_lds(lds + (wave + i * NW) * 1024, base, off[i]);
-        else copy_to_lds(lds + (wave + i * NW) * 1024, reinterpret_cast<const char*>(g_zeros), 0u);
-      }
+      if (kMin == kPer || wave < kInstr)
+        copy_to_lds(lds + (wave + i * NW) * 1024,
+                    kc[i] < valid ? base + off[i] : reinterpret_cast<const char*>(g_zeros));
   }
 };
 
@@ -591,18 +598,26 @@ __device__ __forceinline__ void finish_dglu(const DenseArgs& a, int64_t t, int n
 }
 
 // Columns n .. n + 7 of row t, whose accumulators are columns c .. c + 7 of the
-// fp32 row at `row` (a GLU's gate and up blocks of 16 alternate there).
-template <DenseOp OP>
-__device__ __forceinline__ void finish_chunk(const DenseArgs& a, int64_t t, int n, const float* row, int c) {
+// fp32 row at `row` (a GLU's gate and up blocks of 16 alternate there).  KS partial
+// sums of a split k lie `apart` floats from each other and are added in order.
+template <DenseOp OP, int KS = 1>
+__device__ __forceinline__ void finish_chunk(const DenseArgs& a, int64_t t, int n, const float* row, int c, int apart = 0) {
   const bool in = t < a.T && n < a.N;
   const float* p = row + (OP == DENSE_GLU ? (c >> 4) * 32 + (c & 15) : c);
+  auto sum8 = [&](const float* at, float (&v)[8]) {
+#pragma unroll
+    for (int g = 0; g < KS; ++g, at += apart) {
+      const float4 lo = reinterpret_cast<const float4*>(at)[0], hi = reinterpret_cast<const float4*>(at)[1];
+      const float w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = g ? v[e] + w[e] : w[e];
+    }
+  };
   float v[8];
-  *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(p);
-  *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(p + 4);
+  sum8(p, v);
   if constexpr (OP == DENSE_GLU) {
     float u[8];
-    *reinterpret_cast<float4*>(u) = *reinterpret_cast<const float4*>(p + 16);
-    *reinterpret_cast<float4*>(u + 4) = *reinterpret_cast<const float4*>(p + 20);
+    sum8(p + 16, u);
     finish_glu(a, t, n, in, v, u);
   } else if constexpr (OP == DENSE_DGLU) {
     if (in) finish_dglu(a, t, n, v);
@@ -627,23 +642,25 @@ __device__ __forceinline__ void tile_of(int b, int nt, int nn, int& tt, int& tn)
 }  // namespace
 
 // LDS of a tile kernel: the stages of both operands and, after them, the fp32 tile.
-constexpr int tile_lds(int bt, int bn, int nst, int fp8) {
+constexpr int tile_lds(int bt, int bn, int nst, int fp8, int ks = 1) {
   const int stages = nst * ((bt + bn) * 128 + (fp8 ? bt * 4 : 0)), tile = bt * (bn + 4) * 4;
-  return stages > tile ? stages : tile;
+  return ks * (stages > tile ? stages : tile);
 }
 
 // FP8: 0 bf16 operands, 1 e4m3 through the FP8 MFMA, 2 e4m3 widened to bf16.
-// A WT x WN grid of wavefronts, each with FT x FN blocks of 16 x 16 outputs.
+// A WT x WN grid of wavefronts, each with FT x FN blocks of 16 x 16 outputs, KS times: where there are few tiles and
+// their k is long, KS such grids take every KS-th step each and their sums meet at the end.
 // A GLU tile's B rows alternate 16 gate rows and the 16 up rows of the same
 // columns, so that a wavefront holds both products of its columns.
-template <DenseOp OP, int FP8, bool AK, bool BK, int WT, int WN, int FT, int FN, int NST>
+template <DenseOp OP, int FP8, bool AK, bool BK, int WT, int WN, int FT, int FN, int NST, int KS>
 __device__ __forceinline__ void dense_tile(const DenseArgs& a, int block) {
   constexpr int NW = WT * WN, BT = WT * FT * 16, BN = WN * FN * 16;
   constexpr int NO = OP == DENSE_GLU ? BN / 2 : BN;       // output columns per tile
   constexpr int ES = FP8 ? 1 : 2;
   constexpr int kA = BT * 128, kB = BN * 128, kStage = kA + kB + (FP8 ? BT * 4 : 0);
   extern __shared__ __align__(16) char lds[];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = wave_all % NW, share = wave_all / NW;  // wavefront of its share of k
   const int wt = wave / WN, wn = wave % WN;
   const int q4 = (lane >> 4) * 4, ln = lane & 15;
   int tt, tn;
@@ -679,10 +696,12 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int block) {
   const int scales_k = FP8 ? a.K / 128 : 0;
   const char* ps = nullptr;
   if constexpr (FP8)
-    ps = reinterpret_cast<const char*>(a.as + (int64_t)min(t0 + (int)threadIdx.x, a.T - 1) * scales_k);
+    ps = reinterpret_cast<const char*>(a.as + (int64_t)min(t0 + wave * 64 + lane, a.T - 1) * scales_k);
 
-  auto fetch = [&](int k) {      // copies of step k
-    const uint32_t st = lds0 + (k % NST) * kStage;
+  auto fetch = [&](int it) {     // this share's copies of turn `it`: step it * KS + share
+    const int k = it * KS + share;
+    if (KS > 1 && k >= nk) return;
+    const uint32_t st = lds0 + (it % NST * KS + share) * kStage;
     if (FP8 || k < nk - 1 || tail == kstep) {
       oa.copy(st, wave, pa + k * sa);
       ob.copy(st + kA, wave, pb + k * sb);
@@ -712,14 +731,17 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int block) {
     sw1 = OP == DENSE_GLU ? a.bs + (int64_t)((a.N + min(brow, a.N - 1)) / 128) * scales_k : sw0;
   }
 
+  const int turns = (nk + KS - 1) / KS;
 #pragma unroll
-  for (int k = 0; k < NST - 1; ++k)
-    if (k < nk) fetch(k);
-  for (int k = 0; k < nk; ++k) {
-    if (NST > 2 && k + NST - 1 <= nk) wait_stage<(NST - 2) * kCopies>();
+  for (int it = 0; it < NST - 1; ++it)
+    if (it < turns) fetch(it);
+  for (int it = 0; it < turns; ++it) {
+    if (NST > 2 && (it + NST - 1) * KS <= nk) wait_stage<(NST - 2) * kCopies>();
     else wait_stage<0>();
-    const char* st = lds + (k % NST) * kStage;
-    if (k + NST - 1 < nk) fetch(k + NST - 1);
+    const char* st = lds + (it % NST * KS + share) * kStage;
+    if (it + NST - 1 < turns) fetch(it + NST - 1);
+    const int k = it * KS + share;
+    if (KS > 1 && k >= nk) continue;
     if constexpr (FP8) {
       const float* sc = reinterpret_cast<const float*>(st + kA + kB) + wt * FT * 16 + ln;
       const float w0 = sw0[k], w1 = sw1[k];
@@ -785,37 +807,42 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int block) {
   // against bank conflicts), so that each thread finishes 8 consecutive columns
   // with 16-byte loads and stores.
   constexpr int LR = BN + 4;
-  static_assert(BT * LR * 4 <= tile_lds(BT, BN, NST, FP8), "the tile fits the stages' LDS");
+  static_assert(KS * BT * LR * 4 <= tile_lds(BT, BN, NST, FP8, KS), "the tiles fit the stages' LDS");
   float* tile = reinterpret_cast<float*>(lds);
   wait_stage<0>();                                       // the stages have been read
 #pragma unroll
   for (int i = 0; i < FT; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j)
-      *reinterpret_cast<f32x4_t*>(tile + ((wt * FT + i) * 16 + ln) * LR + (wn * FN + j) * 16 + q4) = acc[i][j];
+      *reinterpret_cast<f32x4_t*>(tile + (share * BT + (wt * FT + i) * 16 + ln) * LR + (wn * FN + j) * 16 + q4) = acc[i][j];
   __syncthreads();
   constexpr int kChunks = NO / 8;
   static_assert(BT * kChunks % 64 == 0, "whole wavefronts finish chunks: scale groups stay together");
 #pragma unroll 1
-  for (int idx = threadIdx.x; idx < BT * kChunks; idx += NW * 64) {
+  for (int idx = threadIdx.x; idx < BT * kChunks; idx += KS * NW * 64) {
     const int r = idx / kChunks, c = (idx % kChunks) * 8;
-    finish_chunk<OP>(a, t0 + r, n0 + c, tile + r * LR, c);
+    finish_chunk<OP, KS>(a, t0 + r, n0 + c, tile + r * LR, c, BT * LR);
   }
 }
 
-template <DenseOp OP, int FP8, bool AK, bool BK, int WT, int WN, int FT, int FN, int NST>
-__global__ __launch_bounds__(WT * WN * 64) void dense_tile_kernel(DenseArgs a) {
-  dense_tile<OP, FP8, AK, BK, WT, WN, FT, FN, NST>(a, blockIdx.x);
+template <DenseOp OP, int FP8, bool AK, bool BK, int WT, int WN, int FT, int FN, int NST, int KS>
+__global__ __launch_bounds__(KS * WT * WN * 64) void dense_tile_kernel(DenseArgs a) {
+  dense_tile<OP, FP8, AK, BK, WT, WN, FT, FN, NST, KS>(a, blockIdx.x);
 }
 
-// The three products of the feed-forward gradients in one launch of 64 x 64 tiles: dx's
-// (the longest sums) first, then dw13's and dw2's.
-__global__ __launch_bounds__(256) void dense_grads_kernel(DenseArgs dx, DenseArgs dw13, DenseArgs dw2, int n_dx,
-                                                          int n_dw13) {
-  const int b = blockIdx.x;
-  if (b < n_dx) dense_tile<DENSE_LINEAR, 0, true, false, 2, 2, 2, 2, 2>(dx, b);
-  else if (b < n_dx + n_dw13) dense_tile<DENSE_LINEAR, 0, false, false, 2, 2, 2, 2, 2>(dw13, b - n_dx);
-  else dense_tile<DENSE_LINEAR, 0, false, false, 2, 2, 2, 2, 2>(dw2, b - n_dx - n_dw13);
+// The three products of the feed-forward gradients in one launch of 64 x 64 tiles, the
+// longest sums first: `weights_first` where there are more tokens than dx's 2 * inter terms.
+template <int KS>
+__global__ __launch_bounds__(KS * 256) void dense_grads_kernel(DenseArgs dx, DenseArgs dw13, DenseArgs dw2, int n_dx,
+                                                               int n_dw13, int n_dw2, int weights_first) {
+  int b = blockIdx.x;
+  if (weights_first) b = b < n_dw13 + n_dw2 ? b + n_dx : b - n_dw13 - n_dw2;
+  if (b < n_dx) {
+    dense_tile<DENSE_LINEAR, 0, true, false, 2, 2, 2, 2, 2, KS>(dx, b);
+  } else {
+    const bool first = b < n_dx + n_dw13;
+    dense_tile<DENSE_LINEAR, 0, false, false, 2, 2, 2, 2, 2, KS>(first ? dw13 : dw2, b - n_dx - (first ? 0 : n_dw13));
+  }
 }
 
 // The large bf16 tile: 256 rows of A by 32 FN (128, 192 or 256) of B, eight wavefronts as
@@ -850,6 +877,8 @@ __global__ __launch_bounds__(512) void dense_pair_kernel(DenseArgs a) {
     return (int64_t)min(r, a.N - 1 - n0);
   }, n0, a.N);
   if (OP == DENSE_GLU && (wave & 2)) pb += (int64_t)a.N * ldb;
+  pa = uniform(pa);
+  pb = uniform(pb);
   Frags<BT, AK, FT> fa;
   Frags<BN, BK, FN> fb;
   fa.init(wt * FT * 16, lane);
@@ -1055,14 +1084,14 @@ __global__ __launch_bounds__(RW * KW * 64) void dense_few_kernel(DenseArgs a) {
 
 namespace {
 
-template <DenseOp OP, int FP8, bool AK, bool BK, int WT, int WN, int FT, int FN, int NST>
+template <DenseOp OP, int FP8, bool AK, bool BK, int WT, int WN, int FT, int FN, int NST, int KS = 1>
 void launch_tile(const DenseArgs& a, hipStream_t s) {
   constexpr int BT = WT * FT * 16, BN = WN * FN * 16, NO = OP == DENSE_GLU ? BN / 2 : BN;
-  constexpr size_t kLds = tile_lds(BT, BN, NST, FP8);
+  constexpr size_t kLds = tile_lds(BT, BN, NST, FP8, KS);
   static_assert(kLds <= 160 * 1024, "LDS of one workgroup");
   const int64_t tiles = (int64_t)((a.T + BT - 1) / BT) * ((a.N + NO - 1) / NO);
-  auto k = dense_tile_kernel<OP, FP8, AK, BK, WT, WN, FT, FN, NST>;
-  k<<<dim3((unsigned)tiles), WT * WN * 64, kLds, s>>>(a);
+  auto k = dense_tile_kernel<OP, FP8, AK, BK, WT, WN, FT, FN, NST, KS>;
+  k<<<dim3((unsigned)tiles), KS * WT * WN * 64, kLds, s>>>(a);
 }
 
 }  // namespace
@@ -1143,8 +1172,11 @@ static void launch_sized(const DenseArgs& a, hipStream_t s) {
     launch_tile<OP, FP8, AK, BK, 2, 2, 2, 2, 2>(a, s);
   } else if (tiles(64, 64) > 128) {
     launch_tile<OP, FP8, AK, BK, 2, 2, 2, 2, 4>(a, s);
+  } else if (OP == DENSE_GLU || tiles(32, 32) <= 256) {
+    // few tiles: their k in four shares (100 x 2048 x 6144: 20.2 -> 13.6 us)
+    launch_tile<OP, FP8, AK, BK, 2, 2, 1, OP == DENSE_GLU ? 2 : 1, 3, 4>(a, s);
   } else {
-    launch_tile<OP, FP8, AK, BK, 2, 2, 1, OP == DENSE_GLU ? 2 : 1, 4>(a, s);
+    launch_tile<OP, FP8, AK, BK, 2, 2, 1, OP == DENSE_GLU ? 2 : 1, 2, 4>(a, s);
   }
 }
 
@@ -1165,11 +1197,23 @@ void launch_dense_grads(const DenseArgs* dx, const DenseArgs* dw13, const DenseA
   auto tiles = [](const DenseArgs& a, int side) {
     return (int64_t)((a.T + side - 1) / side) * ((a.N + side - 1) / side);
   };
-  // Where none fills the units with larger tiles, one launch (257 x 2048 x 768: 22 us of launches one after
-  // another become 13); larger ones go by themselves, each with the tile it is best with.
-  if (dx && dw13 && dw2 && dx->K > 0 && tiles(*dx, 128) < 256 && tiles(*dw13, 128) < 256 && tiles(*dw2, 128) < 256) {
-    const int n0 = (int)tiles(*dx, 64), n1 = (int)tiles(*dw13, 64), n2 = (int)tiles(*dw2, 64);
-    dense_grads_kernel<<<dim3(n0 + n1 + n2), 256, tile_lds(64, 64, 2, 0), s>>>(*dx, *dw13, *dw2, n0, n1);
+  // Where none fills the units with larger tiles, one launch (257 x 2048 x 768: 16 us for what took 22 in three);
+  // larger ones go by themselves, each with the tile it is best with.  So does dx if its tiles are few and its
+  // sums long (29 x 216 x 2512: 38 -> 24 us): by itself its k is split.
+  if (dw13 && dw2 && (!dx || tiles(*dx, 128) < 256) && tiles(*dw13, 128) < 256 && tiles(*dw2, 128) < 256) {
+    if (dx && tiles(*dx, 64) <= 128 && dx->K >= 1024) {
+      launch_dense(DENSE_LINEAR, false, true, false, *dx, s);
+      dx = nullptr;
+    }
+    const int n0 = dx ? (int)tiles(*dx, 64) : 0, n1 = (int)tiles(*dw13, 64), n2 = (int)tiles(*dw2, 64);
+    const DenseArgs x = dx ? *dx : *dw13;
+    const int weights_first = dw13->K > x.K;
+    if (n0 + n1 + n2 <= 256)
+      dense_grads_kernel<4><<<dim3(n0 + n1 + n2), 1024, tile_lds(64, 64, 2, 0, 4), s>>>(x, *dw13, *dw2, n0, n1, n2,
+                                                                                     weights_first);
+    else
+      dense_grads_kernel<1><<<dim3(n0 + n1 + n2), 256, tile_lds(64, 64, 2, 0), s>>>(x, *dw13, *dw2, n0, n1, n2,
+                                                                                  weights_first);
     return;
   }
   if (dx) launch_dense(DENSE_LINEAR, false, true, false, *dx, s);

@@ -980,7 +980,7 @@ __global__ __launch_bounds__(512) void dense_pair_kernel(DenseArgs a) {
 // p * 16 / P ...; of the block only the P diagonal squares are used).  One compute
 // unit cannot draw more than some 55 GB/s from memory, so what counts is that the
 // smaller workgroups are P times as many: gate/up 2 x 6144 x 2048 in bf16 for one
-// row, 10.1 us (5.0 TB/s) with P = 4 against 12-14 us with P = 1.  A GLU's fragments
+// row, 10.7 us (4.7 TB/s) with P = 2 or 4 against 13.5 us with P = 1.  A GLU's fragments
 // alternate gate rows and the up rows of the same columns.
 template <DenseOp OP, int FP8, int RW, int KW, int P, int U>
 __global__ __launch_bounds__(RW * KW * 64) void dense_few_kernel(DenseArgs a) {
@@ -1125,21 +1125,41 @@ static void launch_sized(const DenseArgs& a, hipStream_t s) {
       return;
     }
   }
-  if constexpr (AK && BK) {
-    constexpr bool GLU = OP == DENSE_GLU;
-    if (a.T <= 4) {
-      launch_few_n<OP, FP8, GLU ? 2 : 1, GLU ? 2 : 8, 4, 4>(a, s);
+  // Few rows: blocks of 16, 8 or 4 weight rows, for 16, 8 or 4 rows of x.  Fewer weight rows a block spread a small
+  // weight over the units (8 x 2048 x 6144 in bf16: 16 rows 11.8, 8 rows 8.5 us; 1 x 512 x 6144: 9.3, 6.3 and, with
+  // 4, 5.1), more of them use the matrix instructions better (4 x 4096 x 6144: 12.3, 12.6, 14.7; 8 x 3080 x 6144: 12.3,
+  // 14.3).  From 3 rows on the tiles below win where the blocks are more than the units (8 x 6144 x 6144: 21.0 against
+  // 14.4 us) until their own are too (8 x 12288 x 2048: 11.7 against 12.6), and not where their start and end are
+  // most of the time (6 x 4828 x 440: 4.9 against 5.6).
+  if constexpr (OP == DENSE_LINEAR && AK && BK) {
+    if (a.T <= 4 && a.N < 2048) {
+      launch_few_n<OP, FP8, 1, 8, 4, 4>(a, s);
       return;
     }
-    if (a.T <= 8) {
-      launch_few_n<OP, FP8, GLU ? 2 : 1, GLU ? 4 : 8, 2, 4>(a, s);
+    if (a.T <= 8 && a.N < 2560) {
+      launch_few_n<OP, FP8, 1, 8, 2, 4>(a, s);
       return;
     }
-    // Blocks of 16 x 16 outputs, where they are no more than the units (in FP8, two a unit): each streams its 16 weight
-    // rows with eight wavefronts, where a tile's barriers bound it (32 x 2048 x 6144: 13 against 21 us in bf16, 10
-    // against 23 in FP8; 64 rows: 24 against 21, 16 against 23).
-    if ((int64_t)((a.T + 15) / 16) * ((a.N + 15) / 16) <= (FP8 ? 512 : 256)) {
-      launch_few_n<OP, FP8, GLU ? 2 : 1, GLU ? 4 : 8, 1, 4>(a, s);
+    if ((int64_t)((a.T + 15) / 16) * ((a.N + 15) / 16) <= 256 || a.T <= 2 || (a.T <= 8 && (a.N > 8192 || a.K < 1024))) {
+      launch_few_n<OP, FP8, 1, 8, 1, 4>(a, s);
+      return;
+    }
+  }
+  // A GLU reads two weight rows per column, so it needs half the columns (T x I x H = 1 x 1024 x 2048: 4 rows 4.5, 8 rows
+  // 5.3 us; 1 x 2048 x 2048: 5.7, 5.4), and tiles win earlier (8 x 4096 x 2048: 10.5 against 9.2 us; 1 x 6144 x 2048: 10.7
+  // against 11.0) but for short sums (9 x 608 x 984: 4.6 against 6.6; 16 x 4096 x 1024: 6.8 and 6.8; x 2048: 10.6
+  // against 9.1).
+  if constexpr (OP == DENSE_GLU) {
+    if (a.T <= 4 && a.N < 1280) {
+      launch_few_n<OP, FP8, 2, 2, 4, 4>(a, s);
+      return;
+    }
+    if (a.T <= 2 || (a.T <= 8 && a.N < 2560)) {
+      launch_few_n<OP, FP8, 2, 4, 2, 4>(a, s);
+      return;
+    }
+    if (a.K <= 1280 && (int64_t)((a.T + 15) / 16) * ((a.N + 15) / 16) <= 256) {
+      launch_few_n<OP, FP8, 2, 4, 1, 4>(a, s);
       return;
     }
   }
@@ -1169,14 +1189,21 @@ static void launch_sized(const DenseArgs& a, hipStream_t s) {
       launch_tile<OP, FP8, AK, BK, 2, 4, 4, 2, 2>(a, s);
     }
   } else if (tiles(64, 64) > 256) {
+    // less than one 128 x 128 tile a unit: 64 x 64 (1023 x 2880 x 2880: 26.7 against 33.3 us, 512 x 3000 x 2048: 14.7
+    // against 20.9)
     launch_tile<OP, FP8, AK, BK, 2, 2, 2, 2, 2>(a, s);
-  } else if (tiles(64, 64) > 128) {
-    launch_tile<OP, FP8, AK, BK, 2, 2, 2, 2, 4>(a, s);
-  } else if (OP == DENSE_GLU || tiles(32, 32) <= 256) {
-    // few tiles: their k in four shares (100 x 2048 x 6144: 20.2 -> 13.6 us)
-    launch_tile<OP, FP8, AK, BK, 2, 2, 1, OP == DENSE_GLU ? 2 : 1, 3, 4>(a, s);
+  } else if (tiles(64, 64) <= 128 || tiles(32, OP == DENSE_GLU ? 64 : 32) <= 256 ||
+             (FP8 != 0 && OP == DENSE_LINEAR && (a.T <= 32 || a.K >= 6144))) {
+    // few of those too, or few rows: smaller ones, their k in four shares (100 x 2048 x 6144: 30.1 -> 15.0 us, GLU of
+    // 8 x 6144 x 2048: 12.7 -> 11.4).  In FP8 also up to 256, where its long sums wait for single tiles' copies (320 x
+    // 2048 x 8192: 43.8 -> 30.6 us; 320 x 2048 x 4096 is 17.3 against 18.9).
+    if (OP == DENSE_GLU || tiles(32, 32) <= 256)
+      launch_tile<OP, FP8, AK, BK, 2, 2, 1, OP == DENSE_GLU ? 2 : 1, 3, 4>(a, s);
+    else                             // two a unit: two stages each (500 x 1024 x 4096: 20.5 -> 17.0 us)
+      launch_tile<OP, FP8, AK, BK, 2, 2, 1, OP == DENSE_GLU ? 2 : 1, 2, 4>(a, s);
   } else {
-    launch_tile<OP, FP8, AK, BK, 2, 2, 1, OP == DENSE_GLU ? 2 : 1, 2, 4>(a, s);
+    // one a unit: four stages (320 x 2048 x 4096: 32.5 -> 21.8 us; of 2048 k 11.5 -> 12.5)
+    launch_tile<OP, FP8, AK, BK, 2, 2, 2, 2, 4>(a, s);
   }
 }
 

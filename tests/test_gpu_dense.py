@@ -181,6 +181,30 @@ def test_rmsnorm_of_large_values(H):
     ok()
 
 
+@pytest.mark.parametrize("H", [256, 2048])
+@pytest.mark.parametrize("eps", [0.0, 1e-30])
+def test_rmsnorm_of_small_values(H, eps):
+    """Squares below fp32's range count where eps does not cover them; ordinary rows beside them, and a row of zeros
+    under a positive eps, are as they were."""
+    rng = np.random.default_rng(H + 1)
+    a = rng.standard_normal((6, H))
+    a[1] *= 1e-30
+    a[2] *= 1e-36
+    a[3] *= 1e-14
+    if eps:
+        a[4] = 0
+    x, xv = _bf(a)
+    w, wv = _bf(1 + 0.1 * rng.standard_normal(H))
+    _, y = dense.rmsnorm(xv, None, wv, eps)
+    out, ok = _padded(6, H)
+    pe.rmsnorm(x, w, eps, out)
+    torch.cuda.synchronize()
+    # as for large values: the scalings by powers of two are exact, and the scaled squares of bf16 numbers are normal
+    # (2^-133 at least becomes 2^-106)
+    _within(_np(out), y, np.abs(y) * (BF + (H / 2 + 20) * 2.0 ** -24) + 1e-40, "y")
+    ok()
+
+
 # ------------------------------------------------------------------ routing
 
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (5, 7, 7), (4, 128, 8), (3, 64, 6), (9, 65, 3), (33, 32, 4),

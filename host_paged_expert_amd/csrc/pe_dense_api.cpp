@@ -275,6 +275,8 @@ int pe_ffn_backward(int device, int act, const void* dy, int64_t lddy, const voi
   PE_TRY(check_act(act, false));
   if (H % 8 || I % 8)
     return fail(PE_ERR_INVALID_ARG, "hidden and inter must be multiples of 8");
+  if (H >= kMaxStride || I >= kMaxStride / 2)        // rows of dy and gu, also where T = 0 leaves those unread
+    return fail(PE_ERR_INVALID_ARG, "hidden=%d or 2 * inter=2 * %d is not below 2^22", H, I);
   if (!dx && !dw13 && !dw2) return fail(PE_ERR_INVALID_ARG, "no gradient is asked for");
   const Mat mdy{"dy", dy, T, H, lddy, 2, 16}, mx{"x", x, T, H, ldx, 2, 16}, mgu{"gu", gu, T, 2 * (int64_t)I, 2 * (int64_t)I, 2, 16};
   const Mat mw13{"w13", w13, 2 * (int64_t)I, H, H, 2, 16}, mw2{"w2", w2, H, I, I, 2, 16};

@@ -111,3 +111,12 @@ def test_tensor_functions_check_their_tensors():
         pe.linear(x, None, x)
     with pytest.raises(AttributeError):
         pe.no_such_function
+
+
+@pytest.mark.parametrize("kw", [dict(inter=2 ** 30, dw2=None), dict(inter=2 ** 21, dw2=None),
+                                dict(hidden=2 ** 22, dw13=None)], ids=str)
+def test_backward_of_no_tokens_refuses_sizes_beyond_a_row(kw):
+    """The bounds on rows hold although T = 0 leaves most of them unread: 2 * inter rows of dw13 are counted in 32 bits."""
+    with pytest.raises(pe.PEError) as ei:
+        _back(T=0, **kw)
+    assert ei.value.code == pe.PE_ERR_INVALID_ARG

@@ -16,6 +16,7 @@ from . import _binding as b
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
+_MAX = 2 ** 31 - 1                        # the C entry points' sizes are ints (and bounded below that); ctypes would wrap
 
 
 def _plain(t, dtype, shape, d):
@@ -72,6 +73,8 @@ def _left(name, t):
     if not t.is_cuda or t.dim() != 2:
         raise ValueError("%s must be a matrix on the GPU (got shape %s on %s)" % (name, tuple(t.shape), t.device))
     T, C = t.shape
+    if T > _MAX or C > _MAX:
+        raise ValueError("%s is too large: %s" % (name, tuple(t.shape)))
     return T, C, t.get_device()
 
 
@@ -110,6 +113,8 @@ def route(logits, topk_ids, topk_w, scoring="softmax", renormalize=True, scale=1
     if not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != 2:
         raise ValueError("topk_ids must be a [T, k] tensor")
     k = topk_ids.shape[1]
+    if k > _MAX:
+        raise ValueError("topk_ids is too large: %s" % (tuple(topk_ids.shape),))
     ids = _need("topk_ids", topk_ids, _I32, (T, k), d)
     w = _need("topk_w", topk_w, _F32, (T, k), d)
     return b.check(b.lib().pe_route(d, logits.data_ptr(), ldl, T, E, k, _choice("scoring", scoring, b.SCORES),
@@ -134,6 +139,8 @@ def linear(x, w, out, x_scales=None, w_scales=None, bias=None, act="none", resid
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("w must be a [N, K] tensor")
     N = w.shape[0]
+    if N > _MAX:
+        raise ValueError("w is too large: %s" % (tuple(w.shape),))
     T, K, d, wtype, ldx, wp, xs, ws = _operands(x, w, x_scales, w_scales, N)
     bp = _opt("bias", bias, _BF16, (N,), d)
     ldr, r = 0, None
@@ -156,6 +163,8 @@ def glu(x, w13, out, x_scales=None, w_scales=None, out_scales=None, act="silu", 
     if not isinstance(out, torch.Tensor) or out.dim() != 2:
         raise ValueError("out must be a [T, I] tensor")
     I = out.shape[1]
+    if I > _MAX:
+        raise ValueError("out is too large: %s" % (tuple(out.shape),))
     T, H, d, wtype, ldx, wp, xs, ws = _operands(x, w13, x_scales, w_scales, 2 * I)
     if out_scales is None:
         ldh, hs = _ld("out", out, _BF16, (T, I), d), None
@@ -174,6 +183,8 @@ def ffn_backward(dy, x, gu, w13, w2, dgu, h=None, dx=None, dw13=None, dw2=None, 
     if not isinstance(w2, torch.Tensor) or w2.dim() != 2:
         raise ValueError("w2 must be a [H, I] tensor")
     I = w2.shape[1]
+    if I > _MAX:
+        raise ValueError("w2 is too large: %s" % (tuple(w2.shape),))
     lddy = _ld("dy", dy, _BF16, (T, H), d)
     ldx = lddx = 0
     xp = dxp = None

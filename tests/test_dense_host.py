@@ -120,3 +120,28 @@ def test_backward_of_no_tokens_refuses_sizes_beyond_a_row(kw):
     with pytest.raises(pe.PEError) as ei:
         _back(T=0, **kw)
     assert ei.value.code == pe.PE_ERR_INVALID_ARG
+
+
+def test_tensor_functions_refuse_sizes_that_would_wrap():
+    """2^32 + 4 rows are not 4 rows, nor 2^32 + 8 columns 8: nothing is launched for them."""
+    torch = pytest.importorskip("torch")
+
+    class OnGpu(torch.Tensor):                       # sizes of a tensor that nothing has to hold
+        is_cuda = True
+
+        def get_device(self):
+            return 0
+
+    def t(*shape, dtype=torch.bfloat16):
+        return torch.empty(shape, dtype=dtype, device="meta").as_subclass(OnGpu)
+
+    n = 2 ** 32
+    for call in (lambda: pe.rmsnorm(t(n + 4, 8), t(8), 1e-6, t(n + 4, 8)),
+                 lambda: pe.route(t(n + 4, 8, dtype=torch.float32), t(n + 4, 2, dtype=torch.int32), t(n + 4, 2)),
+                 lambda: pe.route(t(4, 8, dtype=torch.float32), t(4, n + 2, dtype=torch.int32), t(4, n + 2)),
+                 lambda: pe.linear(t(n + 4, 8), t(16, 8), t(n + 4, 16)),
+                 lambda: pe.linear(t(4, 8), t(n + 16, 8), t(4, n + 16)),
+                 lambda: pe.glu(t(4, 8), t(2 * n + 16, 8), t(4, n + 8)),
+                 lambda: pe.ffn_backward(t(4, 8), None, t(4, 2 * n + 16), None, t(8, n + 8), t(4, 2 * n + 16))):
+        with pytest.raises(ValueError, match="too large"):
+            call()

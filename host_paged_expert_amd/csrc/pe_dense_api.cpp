@@ -41,7 +41,13 @@ int check_mat(const Mat& m, bool optional) {
 }
 
 bool overlap(const Mat& a, const Mat& b) {
-  return a.p && b.p && (double)(uintptr_t)a.p < b.end() && (double)(uintptr_t)b.p < a.end();
+  if (!a.p || !b.p || (double)(uintptr_t)a.p >= b.end() || (double)(uintptr_t)b.p >= a.end()) return false;
+  // Column ranges of one wider matrix share no byte although their rows interleave: b's columns lie `at` bytes
+  // behind a's in rows of `stride` bytes.
+  const int64_t stride = a.ld * a.es, len_a = a.cols * a.es, len_b = b.cols * b.es;
+  if (stride != b.ld * b.es) return true;
+  const int64_t at = ((int64_t)((uintptr_t)b.p - (uintptr_t)a.p) % stride + stride) % stride;
+  return at < len_a || at + len_b > stride;
 }
 bool same(const Mat& a, const Mat& b) { return a.p == b.p && a.ld == b.ld && a.es == b.es && a.cols == b.cols; }
 

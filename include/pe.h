@@ -308,9 +308,10 @@ int pe_forward_static(pe_ctx* ctx, int layer, const void* x, const int32_t* topk
  * same time as any other call that does not write its buffers.  Matrices are
  * row-major; a row stride (ld*) counts elements, is at least the row's length
  * and, like every row's length, below 2^22.  Matrices without one are contiguous.  Where nothing else is
- * said, addresses and row strides are multiples of 16 bytes, outputs overlap
- * no input and no other output, T is below 2^24, and T = 0 is a no-op.  Rows are independent
- * of each other.  Sums are fp32. */
+ * said, addresses and row strides are multiples of 16 bytes, outputs share no
+ * byte with an input or another output (column ranges of one wider matrix
+ * share none), T is below 2^24, and T = 0 is a no-op.  Rows are independent of
+ * each other.  Sums are fp32. */
 
 /* activations */
 #define PE_ACT_NONE 0

@@ -145,3 +145,17 @@ def test_tensor_functions_refuse_sizes_that_would_wrap():
                  lambda: pe.ffn_backward(t(4, 8), None, t(4, 2 * n + 16), None, t(8, n + 8), t(4, 2 * n + 16))):
         with pytest.raises(ValueError, match="too large"):
             call()
+
+
+@pytest.mark.parametrize("kw", [dict(y=A[0] + 256, ldx=256, ldy=256), dict(y=A[0] + 254, ldx=256, ldy=256),
+                                dict(y=A[0] + 512 + 312 + 2, ldx=256, ldy=256),
+                                dict(y=A[0] + 256, ldx=256, ldy=512)], ids=str)
+def test_column_ranges_that_share_bytes_are_refused(kw):
+    """x is columns 0 .. 127 of rows of 256 (the last case: y's rows are as far apart as two of x's), y 100 columns
+    of the same rows that begin inside x, or end in the next row's x."""
+    d = dict(K=128, N=100, residual=None, bias=None)
+    if kw["y"] == A[0] + 256 and kw["ldy"] == 256:
+        d["N"], d["ldy"] = 129, 256                  # columns 128 .. 256: one too many
+    with pytest.raises(pe.PEError) as ei:
+        _linear(**dict(kw, **d))
+    assert ei.value.code == pe.PE_ERR_INVALID_ARG and b"overlaps" in pe.pe_last_error().encode()

@@ -366,6 +366,28 @@ def test_linear_into_its_residual():
         assert torch.equal(res, ref)
 
 
+def test_operands_and_outputs_in_columns_of_one_buffer():
+    """x, the residual and y are column ranges of one buffer whose rows interleave; the rest of it stays as it was."""
+    rng = np.random.default_rng(12)
+    T, N, K = 37, 88, 64
+    buf, bufv = _bf(rng.standard_normal((T, 256)))
+    w, wv = _bf(rng.standard_normal((N, K)) / 8)
+    x, r, y = buf[:, :K], buf[:, K:K + N], buf[:, K + N:K + 2 * N]
+    pe.linear(x, w, y, residual=r)
+    torch.cuda.synchronize()
+    got = _np(buf)
+    ref = bufv[:, :K] @ wv.T + bufv[:, K:K + N]
+    tol = np.abs(ref) * BF + (np.abs(bufv[:, :K]) @ np.abs(wv).T + np.abs(bufv[:, K:K + N])) * (K + 2) * 2.0 ** -24 * (1 + BF)
+    _within(got[:, K + N:K + 2 * N], ref, tol, "y")
+    keep = np.r_[0:K + N, K + 2 * N:256]
+    assert (got[:, keep] == bufv[:, keep]).all()
+    g = torch.zeros((T, 64), dtype=torch.bfloat16, device=DEV)
+    pe.rmsnorm(buf[:, :K], w[0], 1e-6, buf[:, 192:256])
+    pe.rmsnorm(x, w[0], 1e-6, g)
+    torch.cuda.synchronize()
+    assert (_np(buf)[:, 192:] == _np(g)).all()
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("T", [2, 40, 150])
 def test_rows_are_independent(T, fp8):

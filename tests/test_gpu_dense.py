@@ -366,6 +366,75 @@ def test_linear_into_its_residual():
         assert torch.equal(res, ref)
 
 
+def _sample(rng, n, count):
+    return np.unique(np.concatenate([[0, n - 1, n // 2], rng.integers(0, n, count)]))
+
+
+# Sizes on both sides of every size at which the products change their way of working: few rows over narrow and wide
+# weights, short and long sums, small, middling and large tiles.
+CHANGES = [(1, 2040, 264), (4, 2056, 264), (2, 2600, 1032), (8, 2552, 136), (8, 2568, 136), (3, 4104, 1040),
+           (7, 4104, 1000), (2, 8200, 72), (8, 8200, 1032), (9, 8200, 72), (16, 4096, 1152), (17, 2048, 1040),
+           (32, 2056, 72), (300, 2048, 6144), (300, 2048, 4096), (500, 1024, 264), (512, 3000, 136),
+           (1800, 2048, 136), (2048, 2048, 256), (2049, 2056, 200), (4099, 2300, 136)]
+
+
+@pytest.mark.parametrize("T,N,K", CHANGES)
+@pytest.mark.parametrize("fp8,dt", [(False, torch.bfloat16), (True, torch.bfloat16), (True, torch.float32)])
+def test_linear_where_its_ways_change(T, N, K, fp8, dt):
+    """A sample of rows and columns, the edges among them, against the oracle."""
+    rng = np.random.default_rng(T + N + K)
+    args, xv, wv, K = _linear_case(T, N, K, fp8, rng)
+    out, ok = _padded(T, N, dt)
+    pe.linear(out=out, **args)
+    torch.cuda.synchronize()
+    ok()
+    rows, cols = _sample(rng, T, 12), _sample(rng, N, 60)
+    xs, ws = xv[rows], wv[cols]
+    y = xs @ ws.T
+    err = (K + 8) * 2.0 ** -24 * (np.abs(xs) @ np.abs(ws).T + np.abs(y))
+    if fp8 and dt == torch.bfloat16:
+        err = err + _aligned(xs, ws)
+    _within(_np(out)[rows][:, cols], y, err + (BF if dt == torch.bfloat16 else 2.0 ** -23) * (np.abs(y) + err), "y")
+
+
+@pytest.mark.parametrize("T,H,I", [(1, 264, 1272), (4, 264, 1288), (2, 136, 2600), (8, 136, 2552), (8, 1040, 2568),
+                                   (3, 2048, 6144), (9, 984, 608), (16, 1288, 2048), (16, 1280, 4096), (32, 72, 8192),
+                                   (40, 72, 4104), (300, 264, 1536), (1000, 136, 3000), (2000, 136, 2048)])
+@pytest.mark.parametrize("wtype,quant", [("bf16", False), ("bf16", True), ("fp8", False), ("fp8", True)])
+def test_glu_where_its_ways_change(T, H, I, wtype, quant):
+    rng = np.random.default_rng(T + H + I)
+    if wtype == "fp8" or quant:
+        I = I // 128 * 128
+    args, xv, wv, H = _linear_case(T, 2 * I, H, wtype == "fp8", rng)
+    args["w13"] = args.pop("w")
+    rows = _sample(rng, T, 8)
+    cols = np.concatenate([np.arange(0, 40), np.arange(I - 40, I)]) if not quant else np.concatenate(
+        [np.arange(0, 128), np.arange(I - 128, I)])        # whole groups where the scales are checked
+    xs, ws = xv[rows], wv[np.concatenate([cols, I + cols])]
+    n = len(cols)
+    g, u, h = dense.glu(xs, ws, "silu")
+    wide = quant or wtype == "bf16"
+    mag = np.abs(xs) @ np.abs(ws).T * (H + 8) * 2.0 ** -24 + (0.0 if wide else _aligned(xs, ws))
+    ag = np.abs(dense.act(g, "silu"))
+    err = (1.13 * mag[:, :n] + FN * ag) * (np.abs(u) + mag[:, n:]) + ag * mag[:, n:] + 2.0 ** -23 * np.abs(h)
+    if not quant:
+        out, ok = _padded(T, I)
+        pe.glu(out=out, **args)
+        torch.cuda.synchronize()
+        ok()
+        _within(_np(out)[rows][:, cols], h, err + BF * (np.abs(h) + err), "h")
+        return
+    out = torch.zeros((T, I), dtype=torch.float8_e4m3fn, device=DEV)
+    sc = torch.zeros((T, I // 128), device=DEV)
+    pe.glu(out=out, out_scales=sc, **args)
+    torch.cuda.synchronize()
+    got_s = _np(sc)[rows][:, [0, -1]]
+    want = dense.group_scales(h)
+    _within(got_s, want, err.reshape(len(rows), 2, 128).max(2) / 448 + want * 2.0 ** -22, "scales")
+    got = dense.dequant_rows(_codes(out)[rows][:, cols], got_s)
+    _within(got, h, err + F8 * (np.abs(h) + err) * (1 + 2.0 ** -20) + np.repeat(got_s, 128, 1) * 2.0 ** -9.9, "h")
+
+
 def test_operands_and_outputs_in_columns_of_one_buffer():
     """x, the residual and y are column ranges of one buffer whose rows interleave; the rest of it stays as it was."""
     rng = np.random.default_rng(12)

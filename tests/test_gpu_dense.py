@@ -586,6 +586,21 @@ def test_ffn_backward(T, H, I, act):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T,H,I", [(5, 376, 1744), (132, 1184, 1456), (257, 2048, 768), (2169, 472, 504), (40, 720, 776),
+                                   (691, 1000, 1000), (1100, 1024, 128)])
+def test_ffn_backward_where_its_launches_change(T, H, I):
+    """Few or many tiles in each of the three products, short and long sums, in one launch or apart."""
+    dev, val = _backward_case(T, H, I, "silu", T + I)
+    x, w13, w2, dy, gu = dev
+    refs, tols = _backward_bounds(*val, "silu")
+    dgu, h = (torch.empty(s, dtype=torch.bfloat16, device=DEV) for s in ((T, 2 * I), (T, I)))
+    out = [torch.full(s, GUARD, dtype=torch.bfloat16, device=DEV) for s in ((T, H), (2 * I, H), (H, I))]
+    pe.ffn_backward(dy, x, gu, w13, w2, dgu, h, dx=out[0], dw13=out[1], dw2=out[2])
+    torch.cuda.synchronize()
+    for name, got, ref, tol in zip(("dx", "dw13", "dw2"), out, refs, tols):
+        _within(_np(got), ref, tol, name)
+
+
 def test_ffn_backward_of_no_tokens():
     H, I = 64, 32
     e = lambda *s: torch.empty(s, dtype=torch.bfloat16, device=DEV)          # noqa: E731

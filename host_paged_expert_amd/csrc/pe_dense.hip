@@ -1168,8 +1168,10 @@ static void launch_sized(const DenseArgs& a, hipStream_t s) {
   if (tiles(128, 128) >= 256) {
     // The fewest rounds of tiles over the 256 units, each in the time of a 256 x 256 tile's (us for one round of
     // 4096 k: 99 with K-major operands, 98 with both k-slow): 256 x 192 takes 0.75 (0.86), 256 x 128 0.62 (0.72),
-    // and two 128 x 128 a unit 0.68 (0.62).  Not for the gradient of h: there the epilogue's bytes weigh as much,
-    // and the smaller tiles of two workgroups a unit overlap them (4096 x 6144 x 2048: 144 against 164 us).
+    // and two 128 x 128 a unit 0.68 (0.62).  Of K-major operands also two 128 x 96 a unit, 0.53 (2048 x 2880 x 2880:
+    // 36.0 us, as 256 x 128 40.9), and two 64 x 128, three stages deep, if they are all of it, 0.42 (2048 x 2048 x 6144:
+    // 60.9 us, as 256 x 128 74.3).  Not for the gradient of h: there the epilogue's bytes weigh as much, and the
+    // smaller tiles of two workgroups a unit overlap them (4096 x 6144 x 2048: 144 against 164 us).
     if constexpr (FP8 == 0 && OP != DENSE_DGLU) {
       auto rounds = [](int64_t n, int64_t per) { return (float)((n + per - 1) / per); };
       constexpr bool slow = !AK && !BK;
@@ -1177,6 +1179,17 @@ static void launch_sized(const DenseArgs& a, hipStream_t s) {
       const float c128 = (slow ? 0.72f : 0.62f) * rounds(tiles(256, 128), 256);
       const float small = (slow ? 0.62f : 0.68f) * rounds(tiles(128, 128), 512);
       const float best = std::min(std::min(c256, c192), std::min(c128, small));
+      if constexpr (AK && BK) {
+        const float c96 = 0.53f * rounds(tiles(128, 96), 512);
+        if (tiles(64, 128) <= 512) {   // (none of the others takes less)
+          launch_tile<OP, FP8, AK, BK, 2, 2, 2, 4, 3>(a, s);
+          return;
+        }
+        if (c96 < best) {
+          launch_tile<OP, FP8, AK, BK, 2, 2, 4, 3, 2>(a, s);
+          return;
+        }
+      }
       if (best == c256) launch_pair<OP, AK, BK, 8>(a, s);
       else if (best == c192) launch_pair<OP, AK, BK, 6>(a, s);
       else if (best == c128) launch_pair<OP, AK, BK, 4>(a, s);
@@ -1191,8 +1204,20 @@ static void launch_sized(const DenseArgs& a, hipStream_t s) {
       launch_tile<OP, FP8, AK, BK, 2, 4, 4, 2, 2>(a, s);
     }
   } else if (tiles(64, 64) > 256) {
-    // less than one 128 x 128 tile a unit: 64 x 64 (1023 x 2880 x 2880: 26.7 against 33.3 us, 512 x 3000 x 2048: 14.7
-    // against 20.9)
+    // less than one 128 x 128 tile a unit: 64 x 64 (512 x 3000 x 2048: 14.7 against 20.9 us).  Of K-major bf16 operands,
+    // where those are more than two a unit, two of 64 x 96 (1023 x 2880 x 2880: 28.5 -> 26.0 us, 1300 x 2048 x 5000: 67.4 ->
+    // 57.9), and where they are not, four stages for long sums, which leave the caches (400 x 2880 x 2880: 24.7 -> 18.8 us,
+    // 1024 x 2048 x 6144: 49.4 -> 40.0; of 2048 k 15.3 -> 15.7).
+    if constexpr (FP8 == 0 && AK && BK) {
+      if (tiles(64, 64) <= 512 && a.K > 2560) {
+        launch_tile<OP, FP8, AK, BK, 2, 2, 2, 2, 4>(a, s);
+        return;
+      }
+      if (tiles(64, 64) > 512 && tiles(64, 96) <= 512) {
+        launch_tile<OP, FP8, AK, BK, 2, 2, 2, 3, 4>(a, s);
+        return;
+      }
+    }
     launch_tile<OP, FP8, AK, BK, 2, 2, 2, 2, 2>(a, s);
   } else if (tiles(64, 64) <= 128 || tiles(32, OP == DENSE_GLU ? 64 : 32) <= 256 ||
              (FP8 != 0 && OP == DENSE_LINEAR && (a.T <= 32 || a.K >= 6144))) {

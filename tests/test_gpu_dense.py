@@ -375,7 +375,8 @@ def _sample(rng, n, count):
 CHANGES = [(1, 2040, 264), (4, 2056, 264), (2, 2600, 1032), (8, 2552, 136), (8, 2568, 136), (3, 4104, 1040),
            (7, 4104, 1000), (2, 8200, 72), (8, 8200, 1032), (9, 8200, 72), (16, 4096, 1152), (17, 2048, 1040),
            (32, 2056, 72), (300, 2048, 6144), (300, 2048, 4096), (500, 1024, 264), (512, 3000, 136),
-           (1800, 2048, 136), (2048, 2048, 256), (2049, 2056, 200), (4099, 2300, 136)]
+           (1800, 2048, 136), (2048, 2048, 256), (2049, 2056, 200), (4099, 2300, 136), (2040, 2040, 200),
+           (2048, 2880, 136), (1023, 2880, 200), (400, 2880, 2888), (1300, 2048, 1032)]
 
 
 @pytest.mark.parametrize("T,N,K", CHANGES)
@@ -399,7 +400,8 @@ def test_linear_where_its_ways_change(T, N, K, fp8, dt):
 
 @pytest.mark.parametrize("T,H,I", [(1, 264, 1272), (4, 264, 1288), (2, 136, 2600), (8, 136, 2552), (8, 1040, 2568),
                                    (3, 2048, 6144), (9, 984, 608), (16, 1288, 2048), (16, 1280, 4096), (32, 72, 8192),
-                                   (40, 72, 4104), (300, 264, 1536), (1000, 136, 3000), (2000, 136, 2048)])
+                                   (40, 72, 4104), (300, 264, 1536), (1000, 136, 3000), (2000, 136, 2048),
+                                   (1000, 136, 1496), (2000, 136, 1016), (2048, 200, 1440), (400, 2888, 1440)])
 @pytest.mark.parametrize("wtype,quant", [("bf16", False), ("bf16", True), ("fp8", False), ("fp8", True)])
 def test_glu_where_its_ways_change(T, H, I, wtype, quant):
     rng = np.random.default_rng(T + H + I)

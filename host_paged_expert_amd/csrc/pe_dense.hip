@@ -157,12 +157,12 @@ __global__ __launch_bounds__(256) void rmsnorm_kernel(NormArgs a) {
   };
   ss = over_row(ss);
   float pre = 1.f, eps = a.eps;
-  const bool large = ss == __builtin_inff(), small = ss < 0x1p-80f && a.eps < 0x1p-60f;
+  const bool large = ss == __builtin_inff() || a.eps > 0x1p100f, small = ss < 0x1p-80f && a.eps < 0x1p-60f;
   if (large || small) {                  // (the same in all of a row's lanes)
-    // Squares past fp32's range: sum those of 2^-70 v, beside which eps is nothing, or, where so small an eps lets
-    // squares below it count, those of 2^80 v.
-    pre = large ? 0x1p-70f : 0x1p80f;
-    eps = large ? 0.f : eps * 0x1p80f * 0x1p80f;
+    // Squares that pass fp32's range, or might with eps: sum those of 2^-75 v (at most 2^106 each, 2^120 in 16384
+    // columns); or, where so small an eps lets squares below the range count, those of 2^80 v.  eps is scaled alike.
+    pre = large ? 0x1p-75f : 0x1p80f;
+    eps = eps * pre * pre;
     ss = 0.f;
 #pragma unroll
     for (int i = 0; i < CH; ++i)

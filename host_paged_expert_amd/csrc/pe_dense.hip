@@ -247,10 +247,16 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     mx = fmaxf(mx, v[j]);
   }
   mx = group_max<LPT>(mx);
-  // softmax numerator of a logit (1 at the maximum, also where that is +infinity), or its sigmoid
+  // softmax numerator of a logit (1 at the maximum, also where that is +infinity), or its sigmoid, of e^-|x| so that small
+  // ones keep what fp32 can hold of them.  Where only the sigmoids' ratios are asked for and all are small, those are
+  // the softmax's numerators' too (e^x / (1 + e^x) without its last term, 2^-28), as long as the largest is not 0 in fp32.
+  const bool sigmoid = a.sigmoid && !(a.renorm && mx < -20.f && mx > -103.5f);
   auto num = [&](float x) {
     if (x == kNone) return 0.f;
-    if (a.sigmoid) return 1.f / (1.f + expf(-x));
+    if (sigmoid) {
+      const float e = expf(-fabsf(x));
+      return (x < 0.f ? e : 1.f) / (1.f + e);
+    }
     return x == mx ? 1.f : expf(x - mx);
   };
   float den = 1.f;

@@ -350,8 +350,8 @@ int pe_rmsnorm(int device, const void* x, int64_t ldx, const void* residual, int
  * ones by ascending id: topk_ids int32 [T, top_k], topk_w fp32 [T, top_k] =
  * scale * score, the score being the softmax over all of the row's logits or
  * the sigmoid.  With `renormalize` the chosen scores are divided by their sum
- * first (left as they are if it is 0).  Logits that are -infinity or NaN are never
- * chosen and weigh nothing; where a row has fewer than top_k others, its last
+ * first (left as they are, 0, if the largest is 0 in fp32: a sigmoid below some
+ * -103).  Logits that are -infinity or NaN are never chosen and weigh nothing; where a row has fewer than top_k others, its last
  * entries get id -1 and weight 0, which pe_forward skips (and counts in
  * bad_ids).  num_experts <= 1024. */
 int pe_route(int device, const float* logits, int64_t ldl, int T, int num_experts, int top_k, int scoring,

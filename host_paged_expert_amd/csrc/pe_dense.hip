@@ -18,13 +18,6 @@ __device__ __forceinline__ float bf16_to_f32(uint16_t b) { return __uint_as_floa
 // fp32 -> bf16 bits, round to nearest even; NaN stays NaN.
 __device__ __forceinline__ uint16_t f32_to_bf16(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
 
-__device__ __forceinline__ float e4m3_to_f32(uint8_t c) { return __builtin_amdgcn_cvt_f32_fp8((int)c, 0); }
-
-// fp32 -> OCP e4m3 code, nearest even; callers keep |v| <= 448 (NaN gives the NaN code).
-__device__ __forceinline__ uint8_t f32_to_e4m3(float v) {
-  return (uint8_t)(__builtin_amdgcn_cvt_pk_fp8_f32(v, 0.f, 0, false) & 0xFF);
-}
-
 constexpr float kE4m3Max = 448.f;
 constexpr float kMinScale = 1.17549435e-38f;   // 2^-126
 
@@ -247,9 +240,10 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     mx = fmaxf(mx, v[j]);
   }
   mx = group_max<LPT>(mx);
-  // softmax numerator of a logit (1 at the maximum, also where that is +infinity), or its sigmoid, of e^-|x| so that small
-  // ones keep what fp32 can hold of them.  Where only the sigmoids' ratios are asked for and all are small, those are
-  // the softmax's numerators' too (e^x / (1 + e^x) without its last term, 2^-28), as long as the largest is not 0 in fp32.
+  // softmax numerator of a logit (1 at the maximum, also where that is +infinity), or its sigmoid, of e^-|x| so that
+  // small ones keep what fp32 can hold of them.  Where only the sigmoids' ratios are asked for and all are small, those
+  // are the softmax's numerators' too (e^x / (1 + e^x) without its last term, 2^-28), as long as the largest is not 0
+  // in fp32.
   const bool sigmoid = a.sigmoid && !(a.renorm && mx < -20.f && mx > -103.5f);
   auto num = [&](float x) {
     if (x == kNone) return 0.f;
@@ -1139,23 +1133,23 @@ static void launch_few_n(const DenseArgs& a, hipStream_t s) {
   dense_few_kernel<OP, FP8, RW, KW, P, U><<<dim3((a.N + NO - 1) / NO, (a.T + NR - 1) / NR), RW * KW * 64, 0, s>>>(a);
 }
 
+// GLU with an e4m3 output: 128 output columns in one tile, a scale group.  The fewest rows that fill the units once
+// (2 x 1536 x 2048 in FP8, by 16, 32, 64 and 128 rows: 256 rows 14.0, 17.1, 23.7, 34.3 us; 1024 rows 43.0, 32.7, 24.9,
+// 35.0; 2048 rows 81.5, 48.3, 46.3, 36.0).
+template <int FP8>
+static void launch_glu_groups(const DenseArgs& a, hipStream_t s) {
+  auto tiles = [&](int rows) { return (int64_t)((a.T + rows - 1) / rows) * (a.N / 128); };
+  if (tiles(16) <= 256) launch_tile<DENSE_GLU, FP8, true, true, 1, 8, 1, 2, 4>(a, s);
+  else if (tiles(32) <= 256) launch_tile<DENSE_GLU, FP8, true, true, 1, 8, 2, 2, 4>(a, s);
+  else if (tiles(64) <= 256) launch_tile<DENSE_GLU, FP8, true, true, 1, 8, 4, 2, 3>(a, s);
+  else launch_tile<DENSE_GLU, FP8, true, true, 2, 4, 4, 4, 3>(a, s);
+}
+
 template <DenseOp OP, int FP8, bool AK, bool BK>
 static void launch_sized(const DenseArgs& a, hipStream_t s) {
   auto tiles = [&](int bt, int bn) {
     return (int64_t)((a.T + bt - 1) / bt) * (((OP == DENSE_GLU ? 2 : 1) * (int64_t)a.N + bn - 1) / bn);
   };
-  if constexpr (OP == DENSE_GLU && FP8 != 1) {
-    // 128 output columns in one tile: a scale group.  The fewest rows that fill the units once (2 x 1536 x 2048 in FP8,
-    // by 16, 32, 64 and 128 rows: 256 rows 14.0, 17.1, 23.7, 34.3 us; 1024 rows 43.0, 32.7, 24.9, 35.0; 2048 rows 81.5,
-    // 48.3, 46.3, 36.0).
-    if (a.hs) {
-      if (tiles(16, 256) <= 256) launch_tile<OP, FP8, AK, BK, 1, 8, 1, 2, 4>(a, s);
-      else if (tiles(32, 256) <= 256) launch_tile<OP, FP8, AK, BK, 1, 8, 2, 2, 4>(a, s);
-      else if (tiles(64, 256) <= 256) launch_tile<OP, FP8, AK, BK, 1, 8, 4, 2, 3>(a, s);
-      else launch_tile<OP, FP8, AK, BK, 2, 4, 4, 4, 3>(a, s);
-      return;
-    }
-  }
   // Few rows: blocks of 16, 8 or 4 weight rows, for 16, 8 or 4 rows of x.  Fewer weight rows a block spread a small
   // weight over the units (8 x 2048 x 6144 in bf16: 16 rows 11.8, 8 rows 8.5 us; 1 x 512 x 6144: 9.3, 6.3 and, with
   // 4, 5.1), more of them use the matrix instructions better (4 x 4096 x 6144: 12.3, 12.6, 14.7; 8 x 3080 x 6144: 12.3,
@@ -1196,18 +1190,19 @@ static void launch_sized(const DenseArgs& a, hipStream_t s) {
   }
   if (tiles(128, 128) >= 256) {
     // The fewest rounds of tiles over the 256 units, each in the time of a 256 x 256 tile's (us for one round of
-    // 4096 k: 99 with K-major operands, 98 with both k-slow): 256 x 192 takes 0.75 (0.86), 256 x 128 0.62 (0.72),
-    // and two 128 x 128 a unit 0.68 (0.62).  Of K-major operands also two 128 x 96 a unit, 0.53 (2048 x 2880 x 2880:
-    // 36.0 us, as 256 x 128 40.9), and two 64 x 128, three stages deep, if they are all of it, 0.42 (2048 x 2048 x 6144:
-    // 60.9 us, as 256 x 128 74.3).  Not for the gradient of h: there the epilogue's bytes weigh as much, and the
-    // smaller tiles of two workgroups a unit overlap them (4096 x 6144 x 2048: 144 against 164 us).
+    // 4096 k: 99 with K-major operands, 98 with both k-slow): 256 x 192 takes 0.75 (0.86), 256 x 128 0.62 (0.72: never
+    // the least), and two 128 x 128 a unit 0.68 (0.62).  Of K-major operands also two 128 x 96 a unit, 0.53 (2048 x
+    // 2880 x 2880: 36.0 us, as 256 x 128 40.9), and two 64 x 128, three stages deep, if they are all of it, 0.42 (2048 x
+    // 2048 x 6144: 60.9 us, as 256 x 128 74.3).  The fractions are measured at these sizes; elsewhere they are a model.
+    // Not for the gradient of h: there the epilogue's bytes weigh as much, and the smaller tiles of two workgroups a
+    // unit overlap them (4096 x 6144 x 2048: 144 against 164 us).
     if constexpr (FP8 == 0 && OP != DENSE_DGLU) {
       auto rounds = [](int64_t n, int64_t per) { return (float)((n + per - 1) / per); };
       constexpr bool slow = !AK && !BK;
       const float c256 = rounds(tiles(256, 256), 256), c192 = (slow ? 0.86f : 0.75f) * rounds(tiles(256, 192), 256);
-      const float c128 = (slow ? 0.72f : 0.62f) * rounds(tiles(256, 128), 256);
+      const float c128 = 0.62f * rounds(tiles(256, 128), 256);
       const float small = (slow ? 0.62f : 0.68f) * rounds(tiles(128, 128), 512);
-      const float best = std::min(std::min(c256, c192), std::min(c128, small));
+      const float best = std::min(std::min(c256, c192), slow ? small : std::min(c128, small));
       if constexpr (AK && BK) {
         const float c96 = 0.53f * rounds(tiles(128, 96), 512);
         if (tiles(64, 128) <= 512) {   // (none of the others takes less)
@@ -1219,10 +1214,21 @@ static void launch_sized(const DenseArgs& a, hipStream_t s) {
           return;
         }
       }
-      if (best == c256) launch_pair<OP, AK, BK, 8>(a, s);
-      else if (best == c192) launch_pair<OP, AK, BK, 6>(a, s);
-      else if (best == c128) launch_pair<OP, AK, BK, 4>(a, s);
-      else launch_tile<OP, FP8, AK, BK, 2, 2, 4, 4, 2>(a, s);
+      if (best == c256) {
+        launch_pair<OP, AK, BK, 8>(a, s);
+        return;
+      }
+      if (best == c192) {
+        launch_pair<OP, AK, BK, 6>(a, s);
+        return;
+      }
+      if constexpr (!slow) {
+        if (best == c128) {
+          launch_pair<OP, AK, BK, 4>(a, s);
+          return;
+        }
+      }
+      launch_tile<OP, FP8, AK, BK, 2, 2, 4, 4, 2>(a, s);
       return;
     }
     if constexpr (FP8 != 0) {
@@ -1264,12 +1270,13 @@ static void launch_sized(const DenseArgs& a, hipStream_t s) {
 }
 
 void launch_dense(DenseOp op, bool fp8, bool ak, bool bk, const DenseArgs& a, hipStream_t s) {
-  const bool wide = a.y_f32 || a.hs;                     // e4m3 operands widened to bf16
-  if (op == DENSE_GLU && fp8 && wide) launch_sized<DENSE_GLU, 2, true, true>(a, s);
+  // e4m3 operands are widened to bf16 where the output or its scales are kept in fp32
+  if (op == DENSE_GLU && a.hs && fp8) launch_glu_groups<2>(a, s);
+  else if (op == DENSE_GLU && a.hs) launch_glu_groups<0>(a, s);
   else if (op == DENSE_GLU && fp8) launch_sized<DENSE_GLU, 1, true, true>(a, s);
   else if (op == DENSE_GLU) launch_sized<DENSE_GLU, 0, true, true>(a, s);
   else if (op == DENSE_DGLU) launch_sized<DENSE_DGLU, 0, true, false>(a, s);
-  else if (fp8 && wide) launch_sized<DENSE_LINEAR, 2, true, true>(a, s);
+  else if (fp8 && a.y_f32) launch_sized<DENSE_LINEAR, 2, true, true>(a, s);
   else if (fp8) launch_sized<DENSE_LINEAR, 1, true, true>(a, s);
   else if (ak && bk) launch_sized<DENSE_LINEAR, 0, true, true>(a, s);
   else if (ak) launch_sized<DENSE_LINEAR, 0, true, false>(a, s);

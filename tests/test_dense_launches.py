@@ -1,4 +1,5 @@
-"""What the dense operators' calls launch, on the CPU (tests/launch_log.py)."""
+"""Which kernels the dense operators' calls launch, on the CPU (tests/launch_log.py): every kernel that the library
+holds for them is one that some call reaches, and every one is run by a GPU test."""
 import pytest
 
 import launch_log
@@ -41,6 +42,16 @@ def calls_of_the_gpu_tests():
     calls += [("backward", T, H, I, "x12") for T, H, I in _params(g.test_ffn_backward_where_its_launches_change, "T,H,I")]
     calls += [("backward",) + c for c in k.BACKWARD]
     return calls
+
+
+def _dense(names):
+    return [n for n in names if n.startswith(("dense_", "rmsnorm_", "route_"))]
+
+
+def test_every_kernel_is_reached_and_tested(shim):
+    kernels, launches = launch_log.launches(shim, calls_of_the_gpu_tests())
+    run = {l[0] for c in launches for l in c}
+    assert len(_dense(kernels)) > 50 and sorted(set(_dense(kernels)) - run) == []
 
 
 def test_launches_are_within_the_device(shim):

@@ -1,6 +1,6 @@
 """The products' larger and rarer kernels against the 64-bit oracle (MI355X only): sizes that lead to each kernel
 that the smaller tests do not reach.  A row of every 32 is checked over all its columns, the edges among them, so that
-every tile has checked elements."""
+every tile has checked elements; tests/test_dense_launches.py holds the list against the library's own choices."""
 import numpy as np
 import pytest
 

@@ -1232,8 +1232,11 @@ static void launch_sized(const DenseArgs& a, hipStream_t s) {
       return;
     }
     if constexpr (FP8 != 0) {
-      // one 128 x 128 tile a unit leaves it waiting for its copies: two of 64 x 128 (2048 x 2048 x 6144: 57 -> 50 us)
-      if (tiles(128, 128) <= 256) launch_tile<OP, FP8, AK, BK, 2, 2, 2, 4, 2>(a, s);
+      // one 128 x 128 tile a unit, or little more, leaves units waiting for their copies: two of 64 x 128 (N = 2048: T =
+      // 2048, 256 tiles, k = 6144 57 -> 50 us; 2176, 272 tiles, k = 2048 21.6 -> 20.7 and k = 6144 57.7 -> 51.2; with
+      // more neither is always better: 2560, 320 tiles, k = 2048 20.9 -> 21.1, k = 6144 55.5 -> 54.1; GLU of 640 x
+      // 3840 x 2048, 300 tiles, 21.0 -> 22.8; 4096, 512 tiles, k = 2048 23.0 -> 33.2)
+      if (tiles(128, 128) <= 288) launch_tile<OP, FP8, AK, BK, 2, 2, 2, 4, 2>(a, s);
       else launch_tile<OP, FP8, AK, BK, 4, 2, 2, 4, 2>(a, s);
     } else {
       launch_tile<OP, FP8, AK, BK, 2, 4, 4, 2, 2>(a, s);
@@ -1258,7 +1261,8 @@ static void launch_sized(const DenseArgs& a, hipStream_t s) {
              (FP8 != 0 && OP == DENSE_LINEAR && (a.T <= 32 || a.K >= 6144))) {
     // few of those too, or few rows: smaller ones, their k in four shares (100 x 2048 x 6144: 30.1 -> 15.0 us, GLU of
     // 8 x 6144 x 2048: 12.7 -> 11.4).  In FP8 also up to 256, where its long sums wait for single tiles' copies (320 x
-    // 2048 x 8192: 43.8 -> 30.6 us; 320 x 2048 x 4096 is 17.3 against 18.9).
+    // 2048 x 8192: 43.8 -> 30.6 us, x 7168 38.2 -> 27.3, x 6144 24.6 -> 24.3; 600 x 1536 x 6144 34.1 -> 27.3; 320 x
+    // 2048 x 4096 is 17.3 against 18.9).
     if (OP == DENSE_GLU || tiles(32, 32) <= 256)
       launch_tile<OP, FP8, AK, BK, 2, 2, 1, OP == DENSE_GLU ? 2 : 1, 3, 4>(a, s);
     else                             // two a unit: two stages each (500 x 1024 x 4096: 20.5 -> 17.0 us)

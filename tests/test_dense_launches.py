@@ -63,3 +63,11 @@ def test_launches_are_within_the_device(shim):
         for name, grid, threads, lds in call:
             assert 64 <= threads <= 1024 and lds <= 160 * 1024, name
             assert min(grid) >= 1 and grid[0] * threads < 2 ** 32 and max(grid[1:]) < 2 ** 16, name
+
+
+def test_fp8_tiles_around_one_a_unit(shim):
+    """The 64 x 128 tile is chosen over a range of sizes, not at one count of tiles: 256 to 288 of 128 x 128."""
+    _, launches = launch_log.launches(shim, [("linear", T, 2048, 256, 1, 0) for T in (1920, 2048, 2049, 2177, 2304, 4096)])
+    names = [c[0][0].split("<")[1] for c in launches]
+    tile, small, large = "0,1,1,1,2,2,2,4,2,1>", "0,1,1,1,2,2,2,2,2,1>", "0,1,1,1,4,2,2,4,2,1>"
+    assert names == [small, tile, tile, tile, tile, large]

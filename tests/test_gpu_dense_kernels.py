@@ -13,7 +13,8 @@ from test_gpu_dense import BF, DEV, FN, _aligned, _bf, _linear_case, _np, _padde
 pytestmark = pytest.mark.gpu
 
 LINEAR = [(1438, 4979, 216), (1603, 4765, 328)]
-GLU = [(3879, 136, 2088, False), (754, 328, 1104, False), (1001, 384, 2048, True)]     # T, hidden, inter, FP8
+GLU = [(3879, 136, 2088, False), (754, 328, 1104, False), (1001, 384, 2048, True),
+       (2177, 256, 1024, True)]       # T, hidden, inter, FP8
 BACKWARD = [(1795, 168, 3224, "x12"), (1795, 168, 3224, "1"), (1795, 168, 3224, "2"), (42, 792, 6056, "x12"),
             (2455, 1592, 144, "x12"), (4099, 2936, 136, "x"), (3313, 2520, 136, "x"), (1552, 4776, 136, "x"),
             (1133, 1896, 1344, "x12"), (1125, 872, 2736, "x12"), (150, 1384, 4920, "x12"), (4095, 2040, 2056, "x12")]

@@ -125,13 +125,14 @@ def _routed(T, E, k, skew, g):
 
 
 def _grouping(ids, E):
-    """Offsets of the experts, the entries in their order and the place of each entry."""
+    """Offsets of the experts, the tokens in their order and the place of each entry."""
     flat = ids.reshape(-1)
     entries = torch.sort(flat, stable=True).indices
     places = torch.empty_like(entries)
     places[entries] = torch.arange(entries.numel(), device=DEV)
     offsets = (flat[None, :] < torch.arange(E + 1, device=DEV)[:, None]).sum(1)
-    return offsets.to(torch.int32), entries.to(torch.int32), places.view(ids.shape).to(torch.int32)
+    rows = torch.div(entries, ids.shape[1], rounding_mode="floor")
+    return offsets.to(torch.int32), rows.to(torch.int32), places.view(ids.shape).to(torch.int32)
 
 
 def prepare(case, seed):
@@ -160,7 +161,7 @@ def prepare(case, seed):
     elif op == "rows":
         i32 = dict(dtype=torch.int32)
         s.update(ids=_routed(c["T"], c["E"], c["k"], c["skew"], g), offsets=empty(c["E"] + 1, **i32),
-                 entries=empty(c["T"] * c["k"], **i32), places=empty(c["T"], c["k"], **i32))
+                 rows=empty(c["T"] * c["k"], **i32), places=empty(c["T"], c["k"], **i32))
     elif op in ("combine", "combine_backward"):
         T, k, H = c["T"], c["k"], c["H"]
         w = torch.rand((T, k), generator=g, device=DEV) + 0.05
@@ -173,8 +174,8 @@ def prepare(case, seed):
     else:
         T, E, k = c["T"], c["E"], c["k"]
         R = T * k
-        offsets, entries, _ = _grouping(_routed(T, E, k, c["skew"], g), E)
-        s.update(offsets=offsets, entries=entries, most=int((offsets[1:] - offsets[:-1]).max()))
+        offsets, rows, _ = _grouping(_routed(T, E, k, c["skew"], g), E)
+        s.update(offsets=offsets, rows=rows, most=int((offsets[1:] - offsets[:-1]).max()))
         if op == "grouped_linear":
             w, ws = weights(E, c["N"], c["K"])
             s.update(x=rnd(R, c["K"]), w=w, ws=ws, bias=rnd(E, c["N"], std=0.1) if c["bias"] else None,
@@ -208,19 +209,18 @@ def _own(s):
         pe.glu_w4(s["x"], s["w"], s["ws"], s["h"], act=c["act"], stream=stream)
         return dict(h=s["h"])
     if op == "rows":
-        pe.group_rows(s["ids"], s["offsets"], s["entries"], s["places"], stream=stream)
-        return dict(offsets=s["offsets"], entries=s["entries"], places=s["places"])
+        pe.group_rows(s["ids"], s["offsets"], s["rows"], s["places"], stream=stream)
+        return dict(offsets=s["offsets"], rows=s["rows"], places=s["places"])
     if op == "grouped_glu":
-        pe.grouped_glu(s["x"], s["w"], s["h"], s["offsets"], entries=s["entries"], top_k=c["k"], w_scales=s["ws"],
-                       act=c["act"], gu=s["gu"], stream=stream)
+        pe.grouped_glu(s["x"], s["w"], s["h"], s["offsets"], rows=s["rows"], w_scales=s["ws"], act=c["act"], gu=s["gu"],
+                       stream=stream)
         return dict(h=s["h"], gu=s["gu"])
     if op == "grouped_linear":
         pe.grouped_linear(s["x"], s["w"], s["y"], s["offsets"], w_scales=s["ws"], bias=s["bias"], stream=stream)
         return dict(y=s["y"])
     if op == "grouped_backward":
-        pe.grouped_ffn_backward(s["dy"], s["x"], s["gu"], s["w13"], s["w2"], s["offsets"], s["dgu"], entries=s["entries"],
-                                top_k=c["k"], h=s["h"], dx=s["dx"], dw13=s["dw13"], dw2=s["dw2"], act=c["act"],
-                                stream=stream)
+        pe.grouped_ffn_backward(s["dy"], s["x"], s["gu"], s["w13"], s["w2"], s["offsets"], s["dgu"], rows=s["rows"],
+                                h=s["h"], dx=s["dx"], dw13=s["dw13"], dw2=s["dw2"], act=c["act"], stream=stream)
         return dict(dx=s["dx"], dw13=s["dw13"], dw2=s["dw2"])
     if op == "combine":
         pe.combine(s["y"], s["places"], s["out"], topk_w=s["w"], residual=s["residual"], stream=stream)
@@ -282,8 +282,8 @@ def _plain(s):
         gu = s["x"].float() @ _weights32(s).t()
         return dict(h=(_act(gu[:, :c["I"]], c["act"]) * gu[:, c["I"]:]).to(bf))
     if op == "rows":
-        offsets, entries, places = _grouping(s["ids"], c["E"])
-        return dict(offsets=offsets, entries=entries, places=places)
+        offsets, rows, places = _grouping(s["ids"], c["E"])
+        return dict(offsets=offsets, rows=rows, places=places)
     if op == "combine":
         y = (s["y"].float()[s["places"].long()] * s["w"][:, :, None]).sum(1)
         return dict(out=(y if s["residual"] is None else y + s["residual"].float()).to(bf))
@@ -296,7 +296,7 @@ def _plain(s):
     if op == "grouped_linear":
         y = torch.bmm(_spread(s["x"], slot, s), _weights32(s).transpose(1, 2).contiguous())[slot]
         return dict(y=(y if s["bias"] is None else y + s["bias"].float()[slot[0]]).to(bf))
-    x = s["x"][s["entries"].long() // c["k"]]
+    x = s["x"][s["rows"].long()]
     if op == "grouped_glu":
         gu = torch.bmm(_spread(x, slot, s), _weights32(s).transpose(1, 2).contiguous())[slot]
         h = _act(gu[:, :c["I"]], c["act"]) * gu[:, c["I"]:]
@@ -389,14 +389,14 @@ def exact(case, seed):
         groups = [[] for _ in range(c["E"])]
         for i, e in enumerate(ids):
             groups[e].append(i)
-        offsets, entries, places = [0], [], [0] * len(ids)
+        offsets, rows, places = [0], [], [0] * len(ids)
         for members in groups:
             for i in members:
-                places[i] = len(entries)
-                entries.append(i)
-            offsets.append(len(entries))
+                places[i] = len(rows)
+                rows.append(i // c["k"])
+            offsets.append(len(rows))
         i32 = dict(dtype=torch.int32)
-        return dict(offsets=torch.tensor(offsets, **i32), entries=torch.tensor(entries, **i32),
+        return dict(offsets=torch.tensor(offsets, **i32), rows=torch.tensor(rows, **i32),
                     places=torch.tensor(places, **i32).view(c["T"], c["k"]))
     if op in ("combine", "combine_backward"):
         w, y, at = s["w"].double(), s["y"].double(), s["places"].long()
@@ -419,7 +419,7 @@ def exact(case, seed):
         return dict(y=y + s["residual"].double() if c["residual"] else y)
 
     bounds = s["offsets"].tolist()
-    token = s["entries"].long() // c["k"]
+    token = s["rows"].long()
 
     def rows(e):
         return slice(bounds[e], bounds[e + 1])

@@ -2,9 +2,11 @@
 
 The work is done by libpe.so (C ABI in include/pe.h, HIP kernels in csrc/).
 This package is its thin ctypes binding plus `PagedMoE`, a small convenience
-owner of one context, and the dense operators around a paged layer on torch
-tensors (dense.py: rmsnorm, route, linear, glu, ffn_backward).  PyTorch is used
-by callers only for device memory and streams.
+owner of one context, and on torch tensors the dense operators around a paged
+layer (dense.py: rmsnorm, route, linear, glu, ffn_backward) and the 4-bit and the
+expert-grouped ones (grouped.py: linear_w4, glu_w4, group_rows, grouped_linear,
+grouped_glu, combine, combine_backward, grouped_ffn_backward).  PyTorch is used by
+callers only for device memory and streams.
 """
 from ._binding import (  # noqa: F401
     LIB_PATH, PEError, lib,
@@ -21,14 +23,24 @@ from ._binding import (  # noqa: F401
     PE_ACT_NONE, PE_ACT_SILU, PE_ACT_GELU, ACTS, PE_Y_BF16, PE_Y_FP32, PE_SCORE_SOFTMAX, PE_SCORE_SIGMOID, SCORES,
     PE_MAX_NORM_HIDDEN,
     pe_rmsnorm, pe_route, pe_linear, pe_glu, pe_ffn_backward,
+    pe_linear_w4, pe_glu_w4, pe_group_rows, pe_grouped_linear, pe_grouped_glu, pe_combine, pe_combine_backward,
+    pe_grouped_ffn_backward,
 )
+
+_DENSE = ("rmsnorm", "route", "linear", "glu", "ffn_backward")
+_GROUPED = ("linear_w4", "glu_w4", "group_rows", "grouped_linear", "grouped_glu", "combine", "combine_backward",
+            "grouped_ffn_backward")
 
 
 def __getattr__(name):
-    # The tensor functions of dense.py import torch, which the rest of the package does without.
-    if name in ("rmsnorm", "route", "linear", "glu", "ffn_backward"):
+    # The tensor functions of dense.py and grouped.py import torch, which the rest of the package does without.
+    if name in _DENSE:
         from . import dense
-        globals().update((n, getattr(dense, n)) for n in ("rmsnorm", "route", "linear", "glu", "ffn_backward"))
+        globals().update((n, getattr(dense, n)) for n in _DENSE)
+        return globals()[name]
+    if name in _GROUPED:
+        from . import grouped
+        globals().update((n, getattr(grouped, n)) for n in _GROUPED)
         return globals()[name]
     raise AttributeError("module %r has no attribute %r" % (__name__, name))
 

@@ -99,6 +99,15 @@ SIGNATURES = {
     "pe_glu": (_i, [_i, _i, _i, _vp, _i64, _vp, _vp, _vp, _i, _i, _i, _vp, _i64, _vp, _vp, _vp]),
     "pe_ffn_backward": (_i, [_i, _i, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _i64, _vp, _vp,
                              _vp]),
+    "pe_linear_w4": (_i, [_i, _i, _vp, _i64, _vp, _vp, _vp, _i, _vp, _i64, _i, _i, _i, _vp, _i64, _i, _vp]),
+    "pe_glu_w4": (_i, [_i, _i, _i, _vp, _i64, _vp, _vp, _i, _i, _i, _vp, _i64, _vp]),
+    "pe_group_rows": (_i, [_i, _vp, _i, _i, _i, _vp, _vp, _vp, _vp]),
+    "pe_grouped_linear": (_i, [_i, _i, _vp, _i64, _i, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _i64, _i, _vp]),
+    "pe_grouped_glu": (_i, [_i, _i, _i, _vp, _i64, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i64, _vp, _vp]),
+    "pe_combine": (_i, [_i, _vp, _i64, _i, _vp, _vp, _vp, _i64, _i, _i, _i, _vp, _i64, _vp]),
+    "pe_combine_backward": (_i, [_i, _vp, _i64, _vp, _vp, _vp, _i64, _i, _i, _i, _i, _vp, _i64, _vp, _vp]),
+    "pe_grouped_ffn_backward": (_i, [_i, _i, _vp, _i64, _vp, _i64, _i, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp,
+                                     _vp, _i64, _vp, _vp, _vp]),
     "pe_strerror": (ctypes.c_char_p, [_i]),
     "pe_last_error": (ctypes.c_char_p, []),
 }
@@ -366,6 +375,52 @@ def pe_ffn_backward(device, act, dy, lddy, x, ldx, gu, w13, w2, T, hidden, inter
     return _check(lib().pe_ffn_backward(device, act, _ptr(dy), lddy, _ptr(x), ldx, _ptr(gu), _ptr(w13), _ptr(w2), T,
                                         hidden, inter, _ptr(dgu), _ptr(h), _ptr(dx), lddx, _ptr(dw13), _ptr(dw2),
                                         _stream(stream)))
+
+
+def pe_linear_w4(device, wtype, x, ldx, w, wscale, bias, act, residual, ldr, T, N, K, y, ldy, ytype, stream=None):
+    return _check(lib().pe_linear_w4(device, wtype, _ptr(x), ldx, _ptr(w), _ptr(wscale), _ptr(bias), act, _ptr(residual),
+                                     ldr, T, N, K, _ptr(y), ldy, ytype, _stream(stream)))
+
+
+def pe_glu_w4(device, wtype, act, x, ldx, w13, s13, T, hidden, inter, h, ldh, stream=None):
+    return _check(lib().pe_glu_w4(device, wtype, act, _ptr(x), ldx, _ptr(w13), _ptr(s13), T, hidden, inter, _ptr(h), ldh,
+                                  _stream(stream)))
+
+
+def pe_group_rows(device, topk_ids, T, top_k, num_experts, offsets, rows, places, stream=None):
+    return _check(lib().pe_group_rows(device, _ptr(topk_ids), T, top_k, num_experts, _ptr(offsets), _ptr(rows),
+                                      _ptr(places), _stream(stream)))
+
+
+def pe_grouped_linear(device, wtype, x, ldx, x_rows, rows, offsets, w, wscale, bias, act, R, num_experts, N, K, y, ldy,
+                      ytype, stream=None):
+    return _check(lib().pe_grouped_linear(device, wtype, _ptr(x), ldx, x_rows, _ptr(rows), _ptr(offsets), _ptr(w),
+                                          _ptr(wscale), _ptr(bias), act, R, num_experts, N, K, _ptr(y), ldy, ytype,
+                                          _stream(stream)))
+
+
+def pe_grouped_glu(device, wtype, act, x, ldx, x_rows, rows, offsets, w13, s13, R, num_experts, hidden, inter, h, ldh,
+                   gu=None, stream=None):
+    return _check(lib().pe_grouped_glu(device, wtype, act, _ptr(x), ldx, x_rows, _ptr(rows), _ptr(offsets), _ptr(w13),
+                                       _ptr(s13), R, num_experts, hidden, inter, _ptr(h), ldh, _ptr(gu), _stream(stream)))
+
+
+def pe_combine(device, y, ldy, R, places, topk_w, residual, ldr, T, top_k, H, out, ldo, stream=None):
+    return _check(lib().pe_combine(device, _ptr(y), ldy, R, _ptr(places), _ptr(topk_w), _ptr(residual), ldr, T, top_k, H,
+                                   _ptr(out), ldo, _stream(stream)))
+
+
+def pe_combine_backward(device, dout, lddo, places, topk_w, y, ldy, R, T, top_k, H, dy, lddy, dtopk_w, stream=None):
+    return _check(lib().pe_combine_backward(device, _ptr(dout), lddo, _ptr(places), _ptr(topk_w), _ptr(y), ldy, R, T,
+                                            top_k, H, _ptr(dy), lddy, _ptr(dtopk_w), _stream(stream)))
+
+
+def pe_grouped_ffn_backward(device, act, dy, lddy, x, ldx, x_rows, rows, offsets, gu, w13, w2, R, num_experts, hidden,
+                            inter, dgu, h, dx, lddx, dw13, dw2, stream=None):
+    return _check(lib().pe_grouped_ffn_backward(device, act, _ptr(dy), lddy, _ptr(x), ldx, x_rows, _ptr(rows),
+                                                _ptr(offsets), _ptr(gu), _ptr(w13), _ptr(w2), R, num_experts, hidden,
+                                                inter, _ptr(dgu), _ptr(h), _ptr(dx), lddx, _ptr(dw13), _ptr(dw2),
+                                                _stream(stream)))
 
 
 def pe_strerror(code):

@@ -1,0 +1,931 @@
+// HIP kernels of the products grouped by expert and of the 4-bit products
+// (gfx950), and of what stands around them: the order of routed entries by
+// expert, the weighted sum of the experts' rows and its gradients.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "../../include/pe.h"
+#include "pe_dense.h"
+#include "pe_grouped.h"
+#include "pe_tiles.h"
+
+namespace pe {
+
+// ------------------------------------------------------------------ order by expert
+//
+// A stable counting sort of the routed ids without scratch memory: the workgroup
+// of expert e counts the ids below e (its first place) and those equal to e, each
+// wavefront over its own stretch of ids, and then numbers the latter in order
+// with ballots.  Every workgroup reads all ids, from L2 after the first.
+template <int NW>
+__global__ __launch_bounds__(NW * 64) void group_rows_kernel(GroupRowsArgs a) {
+  __shared__ int eq_of[NW], lt_of[NW];
+  const int e = blockIdx.x, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int stretch = ((a.n + NW - 1) / NW + 63) / 64 * 64;
+  const int from = wave * stretch, to = min(from + stretch, a.n);
+  int eq = 0, lt = 0;
+#pragma unroll 4
+  for (int i = from + lane; i < to; i += 64) {
+    const uint32_t id = (uint32_t)a.ids[i];           // ids below 0 are above every expert
+    eq += id == (uint32_t)e;
+    lt += id < (uint32_t)e;
+  }
+  auto add = [](int p, int q) { return p + q; };
+  eq = group_reduce<64>(eq, add);
+  lt = group_reduce<64>(lt, add);
+  int base = 0, count = 0;
+  if constexpr (NW > 1) {
+    if (lane == 0) {
+      eq_of[wave] = eq;
+      lt_of[wave] = lt;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      base += lt_of[w] + (w < wave ? eq_of[w] : 0);
+      count += eq_of[w];
+    }
+    if (threadIdx.x == 0) {
+      int first = 0;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) first += lt_of[w];
+      a.offsets[e] = first;
+      if (e == a.E - 1) a.offsets[a.E] = first + count;
+    }
+  } else {
+    base = lt;
+    if (threadIdx.x == 0) {
+      a.offsets[e] = lt;
+      if (e == a.E - 1) a.offsets[a.E] = lt + eq;
+    }
+  }
+  for (int i0 = from; i0 < to; i0 += 64) {
+    const int i = i0 + lane;
+    const int id = i < to ? a.ids[i] : e ? -1 : a.E;
+    const bool mine = i < to && id == e;
+    const uint64_t m = __ballot(mine);
+    if (mine) {
+      const int p = base + __popcll(m & ((1ull << lane) - 1));
+      a.rows[p] = i / a.k;
+      a.places[i] = p;
+    }
+    if (e == 0 && i < to && (uint32_t)id >= (uint32_t)a.E) a.places[i] = -1;
+    base += __popcll(m);
+  }
+}
+
+void launch_group_rows(const GroupRowsArgs& a, hipStream_t s) {
+  if (a.n <= 512) group_rows_kernel<1><<<dim3(a.E), 64, 0, s>>>(a);
+  else if (a.n <= 4096) group_rows_kernel<4><<<dim3(a.E), 256, 0, s>>>(a);
+  else group_rows_kernel<16><<<dim3(a.E), 1024, 0, s>>>(a);
+}
+
+// ------------------------------------------------------------------ sum back to tokens
+//
+// out[t] = sum_j w[t, j] y[places[t, j]] + residual[t], in fp32 and in the order of
+// j: LPR lanes share a token's stretch of 8 LPR columns, each with 8 of them and
+// four rows of y in flight.  Bound by its bytes, each once.
+template <int LPR>
+__global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
+  const int64_t t = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+  const int c = blockIdx.y * LPR + threadIdx.x % LPR;
+  if (t >= a.T || c >= a.H / 8) return;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int j0 = 0; j0 < a.k; j0 += 4) {
+    uint4 y[4];
+    float w[4];
+    bool in[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int at = j0 + j < a.k ? a.places[t * a.k + j0 + j] : -1;
+      in[j] = (uint32_t)at < (uint32_t)a.R;
+      w[j] = in[j] ? a.w ? a.w[t * a.k + j0 + j] : 1.f : 0.f;
+      y[j] = in[j] ? reinterpret_cast<const uint4*>(a.y + at * a.ldy)[c] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (!in[j]) continue;
+      float p[8];
+      widen8(y[j], p);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf(w[j], p[i], v[i]);
+    }
+  }
+  if (a.residual) {
+    float r[8];
+    widen8(reinterpret_cast<const uint4*>(a.residual + t * a.ldr)[c], r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += r[i];
+  }
+  reinterpret_cast<uint4*>(a.out + t * a.ldo)[c] = narrow8(v);
+}
+
+void launch_combine(const CombineArgs& a, hipStream_t s) {
+  const int chunks = a.H / 8;
+  if (chunks <= 64) combine_kernel<64><<<dim3((a.T + 3) / 4, 1), 256, 0, s>>>(a);
+  else if (chunks <= 128) combine_kernel<128><<<dim3((a.T + 1) / 2, 1), 256, 0, s>>>(a);
+  else combine_kernel<256><<<dim3(a.T, (chunks + 255) / 256), 256, 0, s>>>(a);
+}
+
+// dy[places[t, j]] = w[t, j] dout[t] and dw[t, j] = sum_h dout[t, h] y[places[t, j], h]:
+// a wavefront per entry, which shares no sum with another.  Bound by its bytes;
+// dout comes from the caches but for a token's first entry.
+template <bool DY, bool DW>
+__global__ __launch_bounds__(256) void combine_back_kernel(CombineBackArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t i = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (i >= (int64_t)a.T * a.k) return;
+  const int at = a.places[i];
+  if ((uint32_t)at >= (uint32_t)a.R) {
+    if (DW && lane == 0) a.dw[i] = 0.f;
+    return;
+  }
+  const float w = a.w ? a.w[i] : 1.f;
+  const uint4* dout = reinterpret_cast<const uint4*>(a.dout + (int)(i / a.k) * a.lddo);
+  const uint4* y = DW ? reinterpret_cast<const uint4*>(a.y + at * a.ldy) : nullptr;
+  uint4* dy = DY ? reinterpret_cast<uint4*>(a.dy + at * a.lddy) : nullptr;
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int c = lane; c < a.H / 8; c += 64) {
+    float g[8], v[8];
+    widen8(dout[c], g);
+    if constexpr (DW) {
+      widen8(y[c], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] = __builtin_fmaf(g[e], v[e], sum[e]);
+    }
+    if constexpr (DY) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = w * g[e];
+      dy[c] = narrow8(v);
+    }
+  }
+  if constexpr (DW) {
+    const float total = group_sum<64>(((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7])));
+    if (lane == 0) a.dw[i] = total;
+  }
+}
+
+void launch_combine_back(const CombineBackArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)(((int64_t)a.T * a.k + 3) / 4));
+  if (a.dy && a.dw) combine_back_kernel<true, true><<<grid, 256, 0, s>>>(a);
+  else if (a.dy) combine_back_kernel<true, false><<<grid, 256, 0, s>>>(a);
+  else combine_back_kernel<false, true><<<grid, 256, 0, s>>>(a);
+}
+
+// ------------------------------------------------------------------ which rows a workgroup takes
+//
+// Every expert's rows are cut into tiles of their own, numbered expert after
+// expert.  Only the device knows the experts' rows, so the grid holds the most
+// tiles there can be (R / BT + min(E, R)) and each workgroup finds its own, or
+// that it has none: a lane adds up the tiles of its E / 64 experts, one prefix sum over the
+// wavefront gives where they start.  Offsets are held to [0, R], so that whatever they
+// are, no row outside the buffers is touched.
+
+namespace {
+
+struct Tile {
+  int e;          // expert
+  int t0, t1;     // the tile's first row, and one past the expert's last
+  int col;        // tile of columns
+};
+
+// The tile of block `b` among nn tiles of columns; false if there is none.  XCD: neighbouring tiles go to one XCD, an
+// expert's in bands of 8 tiles of rows, column by column (as tile_of does for one matrix).
+template <int BT, bool XCD>
+__device__ __forceinline__ bool find_tile(const GroupedArgs& a, int b, int nn, Tile& t) {
+  constexpr int kBand = 8, kPer = 16;                    // at most 1024 experts
+  if (!a.offsets) {
+    const int nt = (a.R + BT - 1) / BT;
+    int tt = b, tn = 0;
+    if constexpr (XCD) tile_of(b, nt, nn, tt, tn);
+    t = Tile{0, tt * BT, a.R, tn};
+    return true;
+  }
+  const int lane = threadIdx.x & 63, per = (a.E + 63) / 64;
+  int o[kPer + 1];
+#pragma unroll
+  for (int i = 0; i <= kPer; ++i) {
+    o[i] = 0;
+    if (i <= per) o[i] = min(max(a.offsets[min(lane * per + i, a.E)], 0), a.R);
+  }
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (i < per) mine += (max(o[i + 1] - o[i], 0) + BT - 1) / BT;
+  int upto = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(upto, d);
+    if (lane >= d) upto += v;
+  }
+  const int total = __builtin_amdgcn_readlane(upto, 63) * nn;
+  if (b >= total) return false;
+  int q = b;
+  if constexpr (XCD) {
+    constexpr int kXcds = 8;
+    const int xcd = b % kXcds;
+    q = xcd * (total / kXcds) + min(xcd, total % kXcds) + b / kXcds;
+  }
+  const int at = q / nn;                                 // row tile, were the columns the faster index
+  const int owner = __popcll(__ballot(upto <= at));
+  int before = __builtin_amdgcn_readlane(upto - mine, owner), e = owner * per, lo = 0, hi = 0, tiles = 0;
+  bool found = false;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (i < per && !found) {
+      lo = __builtin_amdgcn_readlane(o[i], owner);
+      hi = __builtin_amdgcn_readlane(o[i + 1], owner);
+      tiles = (max(hi - lo, 0) + BT - 1) / BT;
+      found = at < before + tiles;
+      if (!found) {
+        before += tiles;
+        ++e;
+      }
+    }
+  }
+  const int r = q - before * nn;                         // among the expert's own
+  const int band = r / (kBand * nn), rows = min(kBand, tiles - band * kBand), in = r - band * kBand * nn;
+  t = Tile{e, lo + (band * kBand + in % rows) * BT, hi, in / rows};
+  return true;
+}
+
+// The row of x that row p of the output takes.
+__device__ __forceinline__ int64_t x_row(const GroupedArgs& a, int p) {
+  return a.rows ? (int64_t)min((uint32_t)a.rows[p], (uint32_t)(a.x_rows - 1)) : p;
+}
+
+// The K-major operand whose rows lie anywhere: Operand with an address for each lane.
+template <int ROWS, int NW>
+struct RowOperand {
+  static constexpr int kInstr = ROWS / 8, kPer = (kInstr + NW - 1) / NW, kMin = kInstr / NW;
+  static_assert(kInstr % NW == 0 || kPer == 1, "copies divide evenly, or go one each to the first");
+  const char* at[kPer];
+  int kc[kPer];
+
+  // `row(r)`: address of tile row r
+  template <class RowOf>
+  __device__ __forceinline__ void init(int wave, int lane, RowOf row) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int r = 8 * (wave + i * NW) + (lane >> 3);
+      kc[i] = ((lane & 7) ^ ((r >> 1) & 7)) * 16;
+      at[i] = kMin == kPer || wave < kInstr ? row(r) + kc[i] : nullptr;
+    }
+  }
+  // Copy the 128 bytes at byte `from` of each row, of which the first `valid` exist.
+  __device__ __forceinline__ void copy(uint32_t lds, int wave, int64_t from, int valid) const {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (kMin == kPer || wave < kInstr)
+        copy_to_lds(lds + (wave + i * NW) * 1024,
+                    valid == 128 || kc[i] < valid ? at[i] + from : reinterpret_cast<const char*>(g_zeros));
+  }
+};
+
+// The accumulators of a tile go through LDS as fp32 rows (padded by 16 bytes), so that each thread finishes 8 consecutive
+// columns with 16-byte loads and stores.
+template <DenseOp OP, int WT, int WN, int FT, int FN>
+__device__ __forceinline__ void finish_tile(const DenseArgs& a, char* lds, int t0, int n0, const f32x4_t (&acc)[FT][FN]) {
+  constexpr int BT = WT * FT * 16, BN = WN * FN * 16, NO = OP == DENSE_GLU ? BN / 2 : BN, LR = BN + 4, kChunks = NO / 8;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wt = wave / WN, wn = wave % WN;
+  float* tile = reinterpret_cast<float*>(lds);
+  wait_stage<0>();                                       // the stages have been read
+#pragma unroll
+  for (int i = 0; i < FT; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      *reinterpret_cast<f32x4_t*>(tile + ((wt * FT + i) * 16 + (lane & 15)) * LR + (wn * FN + j) * 16 + (lane >> 4) * 4) =
+          acc[i][j];
+  __syncthreads();
+#pragma unroll 1
+  for (int idx = threadIdx.x; idx < BT * kChunks; idx += WT * WN * 64) {
+    const int r = idx / kChunks, c = (idx % kChunks) * 8;
+    finish_chunk<OP>(a, t0 + r, n0 + c, tile + r * LR, c);
+  }
+}
+
+// The arguments of one expert's product.
+__device__ __forceinline__ DenseArgs expert_args(const GroupedArgs& g, int e, int t1, int64_t w_bytes) {
+  DenseArgs a = g.d;
+  a.b = static_cast<const char*>(a.b) + e * w_bytes;
+  if (a.bias) a.bias += (int64_t)e * a.N;
+  a.T = t1;
+  return a;
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------ bf16 products of an expert's rows
+//
+// The tile of pe_dense.hip over an expert's rows: rows of x are fetched through the row list by the copies into LDS
+// themselves, weights K-major (forward) or k-slow (gradients).  An expert's last tile is partly empty; its wavefronts
+// skip the MFMAs of blocks of 16 rows that do not exist.
+template <DenseOp OP, bool BK, int WT, int WN, int FT, int FN, int NST>
+__global__ __launch_bounds__(WT * WN * 64) void grouped_tile_kernel(GroupedArgs g) {
+  constexpr int NW = WT * WN, BT = WT * FT * 16, BN = WN * FN * 16;
+  constexpr int NO = OP == DENSE_GLU ? BN / 2 : BN;
+  constexpr int kA = BT * 128, kB = BN * 128, kStage = kA + kB;
+  extern __shared__ __align__(16) char lds[];
+  Tile tile;
+  if (!find_tile<BT, true>(g, blockIdx.x, (g.d.N + NO - 1) / NO, tile)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wt = wave / WN, wn = wave % WN;
+  const DenseArgs a = expert_args(g, tile.e, tile.t1, (int64_t)(OP == DENSE_GLU ? 2 : 1) * g.d.N * g.d.K * 2);
+  const int t0 = tile.t0, n0 = tile.col * NO;
+  const int64_t ldb = a.ldb * 2;
+  RowOperand<BT, NW> oa;
+  Operand<BN, NW, BK> ob;
+  oa.init(wave, lane, [&](int r) { return static_cast<const char*>(a.a) + x_row(g, min(t0 + r, a.T - 1)) * a.lda * 2; });
+  ob.init(wave, lane, ldb, [&](int r) {
+    if constexpr (OP == DENSE_GLU) return (int64_t)min((r >> 5) * 16 + (r & 15), a.N - 1 - n0);
+    return (int64_t)min(r, a.N - 1 - n0);
+  }, n0, a.N);
+  const char* pb = static_cast<const char*>(a.b) + (BK ? n0 * ldb : 0);
+  static_assert(OP != DENSE_GLU || NW % 4 == 0, "a wavefront's copies stay in one half");
+  if (OP == DENSE_GLU && (wave & 2)) pb += (int64_t)a.N * ldb;
+  pb = uniform(pb);
+  Frags<BT, true, FT> fa;
+  Frags<BN, BK, FN> fb;
+  fa.init(wt * FT * 16, lane);
+  fb.init(wn * FN * 16, lane);
+  const int nk = (a.K + 63) / 64, tail = a.K - (nk - 1) * 64;
+  const int64_t sb = BK ? 128 : 64 * ldb;
+  const uint32_t lds0 = lds_addr(lds);
+  auto fetch = [&](int k) {
+    const uint32_t st = lds0 + k % NST * kStage;
+    const bool whole = k < nk - 1 || tail == 64;
+    oa.copy(st, wave, (int64_t)k * 128, whole ? 128 : tail * 2);
+    if (whole) ob.copy(st + kA, wave, pb + k * sb);
+    else ob.copy_tail(st + kA, wave, pb + k * sb, BK ? tail * 2 : tail);
+  };
+  constexpr int kCopies = decltype(oa)::kMin + decltype(ob)::kMin;
+  f32x4_t acc[FT][FN];
+#pragma unroll
+  for (int i = 0; i < FT; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int blocks = __builtin_amdgcn_readfirstlane((min(BT, a.T - t0) + 15) / 16 - wt * FT);   // this wavefront's that exist
+  auto multiply = [&](const char* st, int upto) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      bf16x8_t af[FT], bf[FN];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) bf[j] = fb.bf16(st + kA, j, s);
+#pragma unroll
+      for (int i = 0; i < FT; ++i)
+        if (i < upto) af[i] = fa.bf16(st, i, s);
+#pragma unroll
+      for (int i = 0; i < FT; ++i)
+        if (i < upto) {
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j], af[i], acc[i][j], 0, 0, 0);
+        }
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < NST - 1; ++k)
+    if (k < nk) fetch(k);
+  for (int k = 0; k < nk; ++k) {
+    if (NST > 2 && k + NST - 1 <= nk) wait_stage<(NST - 2) * kCopies>();
+    else wait_stage<0>();
+    const char* st = lds + k % NST * kStage;
+    if (k + NST - 1 < nk) fetch(k + NST - 1);
+    if (blocks >= FT) multiply(st, FT);
+    else if (blocks > 0) multiply(st, blocks);
+  }
+  finish_tile<OP, WT, WN, FT, FN>(a, lds, t0, n0, acc);
+}
+
+// ------------------------------------------------------------------ weight gradients
+//
+// out[e][m, n] = sum over expert e's rows r of left[r, m] right[r, n]: both operands are k-slow, k being the expert's
+// rows, and an expert without rows gets zeros.  Rows of x come through the row list: its part for the next 32 steps lies
+// in LDS, where the copies of a step find their rows' addresses.
+template <bool GATHER, int WT, int WN, int FT, int FN, int NST>
+__global__ __launch_bounds__(WT * WN * 64) void grouped_weights_kernel(GroupedArgs g) {
+  constexpr int NW = WT * WN, BT = WT * FT * 16, BN = WN * FN * 16, kList = 32;
+  constexpr int kA = BT * 128, kB = BN * 128, kStage = kA + kB;
+  extern __shared__ __align__(16) char lds[];
+  int* list = reinterpret_cast<int*>(lds + NST * kStage);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wt = wave / WN, wn = wave % WN;
+  const int nt = (g.d.T + BT - 1) / BT, nn = (g.d.N + BN - 1) / BN;
+  // neighbouring tiles on one XCD, an expert's all together
+  const int total = g.E * nt * nn, xcd = blockIdx.x % 8;
+  const int q = xcd * (total / 8) + min(xcd, total % 8) + blockIdx.x / 8;
+  const int e = q / (nt * nn), in = q - e * nt * nn;
+  const int band = in / (8 * nn), brows = min(8, nt - band * 8), r = in - band * 8 * nn;
+  const int t0 = (band * 8 + r % brows) * BT, n0 = r / brows * BN;
+  const int r0 = min(max(g.offsets[e], 0), g.R), r1 = min(max(g.offsets[e + 1], 0), g.R);
+  DenseArgs a = g.d;
+  a.y = static_cast<uint16_t*>(a.y) + (int64_t)e * a.T * a.N;
+  const int64_t lda = a.lda * 2, ldb = a.ldb * 2;
+  const int rows = max(r1 - r0, 0), nk = (rows + 63) / 64, tail = rows - (nk - 1) * 64;
+  Operand<BT, NW, false> oa;
+  Operand<BN, NW, false> ob;
+  auto none = [](int) { return (int64_t)0; };
+  oa.init(wave, lane, lda, none, t0, a.T);
+  ob.init(wave, lane, GATHER ? 0 : ldb, none, n0, a.N);
+  const char* pa = uniform(static_cast<const char*>(a.a) + r0 * lda);
+  const char* pb = uniform(static_cast<const char*>(a.b) + (GATHER ? 0 : r0 * ldb));
+  Frags<BT, false, FT> fa;
+  Frags<BN, false, FN> fb;
+  fa.init(wt * FT * 16, lane);
+  fb.init(wn * FN * 16, lane);
+  const uint32_t lds0 = lds_addr(lds);
+  // rows of the steps from k on
+  auto fill = [&](int k) {
+    const int left = min(rows - k * 64, kList * 64);
+    for (int i = threadIdx.x; i < left; i += NW * 64) list[i] = (int)x_row(g, r0 + k * 64 + i);
+  };
+  auto fetch = [&](int k) {
+    const uint32_t st = lds0 + k % NST * kStage;
+    const int valid = k < nk - 1 ? 64 : tail;
+    if (valid == 64) oa.copy(st, wave, pa + k * 64 * lda);
+    else oa.copy_tail(st, wave, pa + k * 64 * lda, valid);
+    if constexpr (GATHER) {
+#pragma unroll
+      for (int i = 0; i < decltype(ob)::kPer; ++i) {
+        if (decltype(ob)::kMin != decltype(ob)::kPer && wave >= decltype(ob)::kInstr) break;
+        const char* p = reinterpret_cast<const char*>(g_zeros);
+        if (ob.kc[i] < valid) p = pb + list[k % kList * 64 + ob.kc[i]] * ldb + ob.off[i];
+        copy_to_lds(st + kA + (wave + i * NW) * 1024, p);
+      }
+    } else {
+      if (valid == 64) ob.copy(st + kA, wave, pb + k * 64 * ldb);
+      else ob.copy_tail(st + kA, wave, pb + k * 64 * ldb, valid);
+    }
+  };
+  constexpr int kCopies = decltype(oa)::kMin + decltype(ob)::kMin;
+  f32x4_t acc[FT][FN];
+#pragma unroll
+  for (int i = 0; i < FT; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  if constexpr (GATHER) {
+    fill(0);
+    __syncthreads();
+  }
+  static_assert(NST - 1 < kList, "the first steps' rows are in the first list");
+#pragma unroll
+  for (int k = 0; k < NST - 1; ++k)
+    if (k < nk) fetch(k);
+  for (int k = 0; k < nk; ++k) {
+    if (NST > 2 && k + NST - 1 <= nk) wait_stage<(NST - 2) * kCopies>();
+    else wait_stage<0>();
+    const char* st = lds + k % NST * kStage;
+    const int next = k + NST - 1;
+    if (next < nk) {
+      if (GATHER && next % kList == 0) {                 // every wavefront has read its rows of the step before
+        fill(next);
+        __syncthreads();
+      }
+      fetch(next);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      bf16x8_t af[FT], bf[FN];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) bf[j] = fb.bf16(st + kA, j, s);
+#pragma unroll
+      for (int i = 0; i < FT; ++i) af[i] = fa.bf16(st, i, s);
+#pragma unroll
+      for (int i = 0; i < FT; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j], af[i], acc[i][j], 0, 0, 0);
+    }
+  }
+  finish_tile<DENSE_LINEAR, WT, WN, FT, FN>(a, lds, t0, n0, acc);
+}
+
+// ------------------------------------------------------------------ 4-bit weights
+//
+// The products sum_k x[k] w[k] take the codes' values as bf16, exactly, and a scale as far out as it is constant:
+//   MXFP4: an E2M1 value times its block's power of two is exact in bf16 (but for products beyond bf16's range, which
+//          are infinite, or below it), so v_cvt_scalef32_pk_bf16_fp4 makes operands that need nothing more.
+//   int4:  the fp16 scale of 128 k multiplies the fp32 sum over them.  The code q (0 .. 15) is an e4m3 number of value
+//          q 2^-9 (denormal below 8), so one v_cvt_scalef32_pk_bf16_fp8 makes two operands from bytes; and since
+//          sum x (q - 8) = sum x q - 8 sum x, the chain of MFMAs starts at -8 sum x, which an MFMA with a constant -8
+//          operand makes, once for all of a tile's weight rows.  Terms are so up to 15 |x| s where |q - 8| s |x| is
+//          meant: the fp32 error is that of sum |x| (q + 8) s.  (Subtracting 8 from the codes first takes twice
+//          the instructions.)
+
+namespace {
+
+template <int WTYPE> constexpr bool kInt4 = WTYPE == PE_W_INT4_G128;
+template <int WTYPE> constexpr bool kMx = WTYPE == PE_W_MXFP4_B32;
+template <int WTYPE> constexpr int kScaleGroup = kInt4<WTYPE> ? 128 : 32;
+
+// Eight codes (the first in the lowest nibble) as bf16: int4 q, MXFP4 the value times `scale`.
+template <int WTYPE>
+__device__ __forceinline__ bf16x8_t decode8(uint32_t d, float scale) {
+  typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
+  if constexpr (kMx<WTYPE>) {
+    const bf16x2_t p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 0);
+    const bf16x2_t p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 1);
+    const bf16x2_t p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 2);
+    const bf16x2_t p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 3);
+    return bf16x8_t{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+  } else {
+    const uint32_t even = d & 0x0F0F0F0Fu, odd = (d >> 4) & 0x0F0F0F0Fu;
+    const uint32_t lo = __builtin_amdgcn_perm(odd, even, 0x05010400u), hi = __builtin_amdgcn_perm(odd, even, 0x07030602u);
+    const bf16x2_t p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false);
+    const bf16x2_t p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true);
+    const bf16x2_t p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false);
+    const bf16x2_t p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true);
+    return bf16x8_t{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+  }
+}
+
+// An E8M0 byte as the fp32 number 2^(e - 127); 255 is NaN.
+__device__ __forceinline__ float e8m0(uint32_t e) {
+  return __uint_as_float(e == 0 ? 0x00400000u : e == 255 ? 0x7FC00000u : e << 23);
+}
+
+__device__ __forceinline__ bf16x8_t minus8() {
+  const __bf16 v = (__bf16)-8.f;
+  return bf16x8_t{v, v, v, v, v, v, v, v};
+}
+
+__device__ __forceinline__ float half_value(uint16_t h) { return (float)__builtin_bit_cast(_Float16, h); }
+
+}  // namespace
+
+// ------------------------------------------------------------------ products of few rows
+//
+// A few rows for each matrix (a decode step): the weights' bytes bound the product, so they stream straight from memory
+// into MFMA operands.  A workgroup takes 16 / P weight rows (of a GLU 16 / P gate rows and their up rows) and 16 / P
+// rows of x, its KW wavefronts every KW-th step of k each with U steps in flight; the partial sums meet in LDS in a
+// fixed order.  A step is 128 bytes of k in bf16 and 64 bytes, 128 k, in 4 bits: a lane's 16 bytes of codes are
+// 32 consecutive k, one MXFP4 block.  P parts of k share the MFMA's 16 x 16 block as in the dense kernel of few rows.
+// x is the first operand, so that a lane's accumulators belong to one weight row and its scale.
+template <DenseOp OP, int WTYPE, int KW, int P, int U>
+__global__ __launch_bounds__(KW * 64) void grouped_few_kernel(GroupedArgs g) {
+  constexpr int NR = 16 / P, F = OP == DENSE_GLU ? 2 : 1;
+  constexpr bool Q = WTYPE != PE_W_BF16;
+  constexpr int kStep = Q ? 128 : 64, kX = Q ? 4 : 2, kW = Q ? 1 : 2;
+  __shared__ f32x4_t red[F][KW][64];
+  Tile tile;
+  if (!find_tile<NR, false>(g, blockIdx.y, 1, tile)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, ln = lane & 15, part = ln / NR, lr = ln % NR;
+  const int K = g.d.K, N = g.d.N;
+  const int64_t row_bytes = Q ? K / 2 : (int64_t)K * 2;
+  const DenseArgs a = expert_args(g, tile.e, tile.t1, F * N * row_bytes);
+  const int n0 = blockIdx.x * NR, t0 = tile.t0;
+  const int nk = (K + kStep - 1) / kStep;
+  const int wrow = min(n0 + lr, N - 1);
+  const char* px = static_cast<const char*>(a.a) + x_row(g, min(t0 + lr, a.T - 1)) * a.lda * 2;
+  const char* pw[F];
+  const uint16_t* s16[F];
+  const uint8_t* s8[F];
+#pragma unroll
+  for (int f = 0; f < F; ++f) {
+    pw[f] = static_cast<const char*>(a.b) + ((int64_t)f * N + wrow) * row_bytes + 16 * q;
+    const int64_t at = ((int64_t)tile.e * F * N + (int64_t)f * N + wrow) * (K / kScaleGroup<WTYPE>);
+    s16[f] = static_cast<const uint16_t*>(g.ws) + at;
+    s8[f] = static_cast<const uint8_t*>(g.ws) + at;
+  }
+  f32x4_t acc[F];
+#pragma unroll
+  for (int f = 0; f < F; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int k0 = wave * P; k0 < nk; k0 += KW * P * U) {
+    uint4 w[U][F][kW], x[U][kX];
+    float s[U][F];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * KW * P + part;
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      if constexpr (Q) {
+        const bool in = k * 128 + 32 * q < K;
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+          w[u][f][0] = in ? *reinterpret_cast<const uint4*>(pw[f] + (int64_t)k * 64) : zero;
+          s[u][f] = 0.f;
+          if (in) s[u][f] = kInt4<WTYPE> ? half_value(s16[f][k]) : e8m0(s8[f][4 * k + q]);
+        }
+#pragma unroll
+        for (int c = 0; c < kX; ++c)
+          x[u][c] = in ? *reinterpret_cast<const uint4*>(px + (int64_t)k * 256 + 64 * q + 16 * c) : zero;
+      } else {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const bool in = k * 64 + 32 * c + 8 * q < K;
+#pragma unroll
+          for (int f = 0; f < F; ++f)
+            w[u][f][c] = in ? *reinterpret_cast<const uint4*>(pw[f] + (int64_t)k * 128 + 64 * c) : zero;
+          x[u][c] = in ? *reinterpret_cast<const uint4*>(px + (int64_t)k * 128 + 64 * c + 16 * q) : zero;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if constexpr (kInt4<WTYPE>) {
+        f32x4_t start = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          start = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x[u][c]), minus8(), start, 0, 0, 0);
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+          const uint32_t d[4] = {w[u][f][0].x, w[u][f][0].y, w[u][f][0].z, w[u][f][0].w};
+          f32x4_t p = start;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x[u][c]), decode8<WTYPE>(d[c], 0.f), p,
+                                                        0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[f][i] = __builtin_fmaf(p[i], s[u][f], acc[f][i]);
+        }
+      } else {
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+#pragma unroll
+          for (int c = 0; c < kX; ++c) {
+            bf16x8_t v;
+            if constexpr (Q) {
+              const uint32_t d[4] = {w[u][f][0].x, w[u][f][0].y, w[u][f][0].z, w[u][f][0].w};
+              v = decode8<WTYPE>(d[c], s[u][f]);
+            } else {
+              v = __builtin_bit_cast(bf16x8_t, w[u][f][c]);
+            }
+            acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x[u][c]), v, acc[f], 0, 0, 0);
+          }
+      }
+    }
+  }
+#pragma unroll
+  for (int f = 0; f < F; ++f) red[f][wave][lane] = acc[f];
+  __syncthreads();
+
+  // Four consecutive columns of one row per thread: their P parts of the KW sums.
+  if (threadIdx.x >= NR * NR / 4) return;
+  const int tr = threadIdx.x / (NR / 4), c4 = threadIdx.x % (NR / 4) * 4;
+  const int t = t0 + tr, n = n0 + c4;
+  if (t >= a.T || n >= N) return;
+  auto sum = [&](int f, float (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = 0.f;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          const int row = p * NR + tr;
+          v[i] += reinterpret_cast<const float*>(&red[f][w][row / 4 * 16 + p * NR + c4 + i])[row % 4];
+        }
+    }
+  };
+  float v[4];
+  sum(0, v);
+  if constexpr (OP == DENSE_GLU) {
+    float u[4];
+    sum(1, u);
+    finish_glu(a, t, n, true, v, u);
+  } else {
+    finish_linear(a, t, n, v);
+  }
+}
+
+// ------------------------------------------------------------------ 4-bit products of many rows
+//
+// The tile kernel with codes for weights: steps of 64 k, x's 128 bytes a row and the codes' 32 copied straight into
+// LDS, the codes decoded by the wavefront that multiplies them.  A row's two 16-byte halves are exchanged in every other
+// eight rows, so that the 16 rows of one read fall on all banks.  The scales of 1024 k lie in LDS as well (int4 as fp32
+// by group, MXFP4 as bytes by row); those of the next 1024 wait in registers while these are used.
+template <DenseOp OP, int WTYPE, int WT, int WN, int FT, int FN, int NST>
+__global__ __launch_bounds__(WT * WN * 64) void quant_tile_kernel(GroupedArgs g) {
+  constexpr int NW = WT * WN, BT = WT * FT * 16, BN = WN * FN * 16, kThreads = NW * 64;
+  constexpr int NO = OP == DENSE_GLU ? BN / 2 : BN;
+  constexpr int kA = BT * 128, kB = BN * 32, kStage = kA + kB;
+  constexpr int kChunk = 16;                             // steps that share a stretch of scales
+  constexpr int kGroups = kInt4<WTYPE> ? 8 : 32;         // scales of a row in it
+  constexpr int kRow = kInt4<WTYPE> ? 4 * BN : 36;       // bytes from group to group, from row to row
+  // scales a thread holds: one fp16 each, or four bytes
+  constexpr int kHeld = BN * kGroups / (kInt4<WTYPE> ? 1 : 4) / kThreads;
+  static_assert(kHeld * kThreads * (kInt4<WTYPE> ? 1 : 4) == BN * kGroups, "threads hold whole shares");
+  extern __shared__ __align__(16) char lds[];
+  char* scales = lds + NST * kStage;
+  Tile tile;
+  if (!find_tile<BT, true>(g, blockIdx.x, (g.d.N + NO - 1) / NO, tile)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wt = wave / WN, wn = wave % WN, q = lane >> 4, ln = lane & 15;
+  constexpr int F = OP == DENSE_GLU ? 2 : 1;
+  const int K = g.d.K, per_row = K / kScaleGroup<WTYPE>;
+  const DenseArgs a = expert_args(g, tile.e, tile.t1, (int64_t)F * g.d.N * (K / 2));
+  const int t0 = tile.t0, n0 = tile.col * NO;
+  // the expert's weight row of tile row r
+  auto w_row = [&](int r) {
+    if constexpr (OP == DENSE_GLU) return (int64_t)min(n0 + (r >> 5) * 16 + (r & 15), a.N - 1) + (r & 16 ? a.N : 0);
+    return (int64_t)min(n0 + r, a.N - 1);
+  };
+  RowOperand<BT, NW> oa;
+  oa.init(wave, lane, [&](int r) { return static_cast<const char*>(a.a) + x_row(g, min(t0 + r, a.T - 1)) * a.lda * 2; });
+  constexpr int kCodes = BN / 32, kCodesPer = (kCodes + NW - 1) / NW, kCodesMin = kCodes / NW;   // 1024-byte copies a step
+  static_assert(kCodes % NW == 0 || kCodesPer == 1, "copies divide evenly, or go one each to the first");
+  const char* codes[kCodesPer];
+  int half[kCodesPer];
+#pragma unroll
+  for (int i = 0; i < kCodesPer; ++i) {
+    const int r = 32 * (wave + i * NW) + (lane >> 1);
+    half[i] = ((lane & 1) ^ ((r >> 3) & 1)) * 16;
+    codes[i] = static_cast<const char*>(a.b) + w_row(min(r, BN - 1)) * (K / 2) + half[i];
+  }
+  Frags<BT, true, FT> fa;
+  fa.init(wt * FT * 16, lane);
+  const int nk = (K + 63) / 64, tail = K - (nk - 1) * 64;
+  const uint32_t lds0 = lds_addr(lds);
+  auto fetch = [&](int k) {
+    const uint32_t st = lds0 + k % NST * kStage;
+    const int valid = k < nk - 1 ? 64 : tail;
+    oa.copy(st, wave, (int64_t)k * 128, valid * 2);
+#pragma unroll
+    for (int i = 0; i < kCodesPer; ++i)
+      if (kCodesMin == kCodesPer || wave < kCodes)
+        copy_to_lds(st + kA + (wave + i * NW) * 1024,
+                    half[i] < valid / 2 ? codes[i] + (int64_t)k * 32 : reinterpret_cast<const char*>(g_zeros));
+  };
+  constexpr int kCopies = decltype(oa)::kMin + kCodesMin;
+  // this thread's scales of chunk c: thread after thread along the rows
+  uint32_t held[kHeld];
+  const bool words = K % 128 == 0;                       // MXFP4 rows of whole words
+  auto hold = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int idx = threadIdx.x + i * kThreads;
+      held[i] = 0;
+      if constexpr (kInt4<WTYPE>) {
+        const int at = c * 8 + idx % 8;
+        if (at < per_row)
+          held[i] = static_cast<const uint16_t*>(g.ws)[((int64_t)tile.e * F * a.N + w_row(idx / 8)) * per_row + at];
+      } else {
+        const int at = c * 32 + idx % 8 * 4;
+        const uint8_t* p = static_cast<const uint8_t*>(g.ws) + ((int64_t)tile.e * F * a.N + w_row(idx / 8)) * per_row + at;
+        if (words) {
+          if (at < per_row) held[i] = *reinterpret_cast<const uint32_t*>(p);
+        } else {
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            if (at + b < per_row) held[i] |= (uint32_t)p[b] << (8 * b);
+        }
+      }
+    }
+  };
+  auto place = [&] {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int idx = threadIdx.x + i * kThreads;
+      if constexpr (kInt4<WTYPE>) *reinterpret_cast<float*>(scales + idx % 8 * kRow + idx / 8 * 4) = half_value((uint16_t)held[i]);
+      else *reinterpret_cast<uint32_t*>(scales + idx / 8 * kRow + idx % 8 * 4) = held[i];
+    }
+  };
+  f32x4_t acc[FT][FN];
+#pragma unroll
+  for (int i = 0; i < FT; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int blocks = __builtin_amdgcn_readfirstlane((min(BT, a.T - t0) + 15) / 16 - wt * FT);
+  auto multiply = [&](int k, int upto) {
+    const char* st = lds + k % NST * kStage;
+    const char* cw = st + kA + (wn * FN * 16 + ln) * 32 + 4 * q;
+    bf16x8_t bf[FN][2];
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint32_t d = *reinterpret_cast<const uint32_t*>(cw + j * 512 + ((s ^ (ln >> 3)) << 4));
+        float scale = 0.f;
+        if constexpr (kMx<WTYPE>)
+          scale = e8m0(*reinterpret_cast<const uint8_t*>(scales + ((wn * FN + j) * 16 + ln) * kRow + k % kChunk * 2 + s));
+        bf[j][s] = decode8<WTYPE>(d, scale);
+      }
+    f32x4_t sc[kInt4<WTYPE> ? FN : 1];
+    if constexpr (kInt4<WTYPE>) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        sc[j] = *reinterpret_cast<const f32x4_t*>(scales + k % kChunk / 2 * kRow + ((wn * FN + j) * 16 + 4 * q) * 4);
+    }
+#pragma unroll
+    for (int i = 0; i < FT; ++i) {
+      if (i >= upto) continue;
+      bf16x8_t af[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) af[s] = fa.bf16(st, i, s);
+      if constexpr (kInt4<WTYPE>) {
+        f32x4_t start = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < 2; ++s) start = __builtin_amdgcn_mfma_f32_16x16x32_bf16(minus8(), af[s], start, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          f32x4_t p = start;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j][s], af[s], p, 0, 0, 0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[e], sc[j][e], acc[i][j][e]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j][s], af[s], acc[i][j], 0, 0, 0);
+      }
+    }
+  };
+  hold(0);
+#pragma unroll
+  for (int k = 0; k < NST - 1; ++k)
+    if (k < nk) fetch(k);
+  for (int k = 0; k < nk; ++k) {
+    if (k % kChunk == 0) {
+      __syncthreads();                                   // the scales before these have been used
+      place();
+    }
+    // (scales being fetched only make this wait for more)
+    if (NST > 2 && k + NST - 1 <= nk) wait_stage<(NST - 2) * kCopies>();
+    else wait_stage<0>();
+    if (k + NST - 1 < nk) fetch(k + NST - 1);
+    if (k % kChunk == 0 && k + kChunk < nk) hold(k / kChunk + 1);
+    if (blocks >= FT) multiply(k, FT);
+    else if (blocks > 0) multiply(k, blocks);
+  }
+  finish_tile<OP, WT, WN, FT, FN>(a, lds, t0, n0, acc);
+}
+
+// ------------------------------------------------------------------ launches
+
+namespace {
+
+// The most tiles of `bt` rows there can be.
+int64_t row_tiles(const GroupedArgs& a, int bt) {
+  return a.offsets ? (int64_t)a.R / bt + std::min(a.E, a.R) : ((int64_t)a.R + bt - 1) / bt;
+}
+
+template <DenseOp OP, bool BK, int WT, int WN, int FT, int FN, int NST>
+void launch_rows(const GroupedArgs& a, hipStream_t s) {
+  constexpr int BT = WT * FT * 16, BN = WN * FN * 16, NO = OP == DENSE_GLU ? BN / 2 : BN;
+  constexpr int kLds = std::max(NST * (BT + BN) * 128, BT * (BN + 4) * 4);
+  static_assert(kLds <= 160 * 1024, "LDS of one workgroup");
+  const int64_t tiles = row_tiles(a, BT) * ((a.d.N + NO - 1) / NO);
+  grouped_tile_kernel<OP, BK, WT, WN, FT, FN, NST><<<dim3((unsigned)tiles), WT * WN * 64, kLds, s>>>(a);
+}
+
+template <DenseOp OP, int WTYPE, int WT, int WN, int FT, int FN, int NST>
+void launch_quant(const GroupedArgs& a, hipStream_t s) {
+  constexpr int BT = WT * FT * 16, BN = WN * FN * 16, NO = OP == DENSE_GLU ? BN / 2 : BN;
+  constexpr int kLds = std::max(NST * (BT * 128 + BN * 32) + BN * (kInt4<WTYPE> ? 32 : 36), BT * (BN + 4) * 4);
+  static_assert(kLds <= 160 * 1024, "LDS of one workgroup");
+  const int64_t tiles = row_tiles(a, BT) * ((a.d.N + NO - 1) / NO);
+  quant_tile_kernel<OP, WTYPE, WT, WN, FT, FN, NST><<<dim3((unsigned)tiles), WT * WN * 64, kLds, s>>>(a);
+}
+
+template <DenseOp OP, int WTYPE, int KW, int P, int U>
+void launch_few(const GroupedArgs& a, hipStream_t s) {
+  constexpr int NR = 16 / P;
+  grouped_few_kernel<OP, WTYPE, KW, P, U>
+      <<<dim3((a.d.N + NR - 1) / NR, (unsigned)row_tiles(a, NR)), KW * 64, 0, s>>>(a);
+}
+
+template <DenseOp OP, int WTYPE>
+void launch_sized(const GroupedArgs& a, hipStream_t s) {
+  const int rows = a.offsets ? a.R / std::min(a.E, a.R) : a.R;    // of a matrix
+  if (rows <= 32 && row_tiles(a, 16) < 65536) {
+    launch_few<OP, WTYPE, 4, 1, 4>(a, s);
+    return;
+  }
+  if constexpr (WTYPE == PE_W_BF16) launch_rows<OP, true, 2, 2, 4, 4, 2>(a, s);
+  else launch_quant<OP, WTYPE, 2, 2, 4, 4, 3>(a, s);
+}
+
+}  // namespace
+
+void launch_grouped(DenseOp op, int wtype, const GroupedArgs& a, hipStream_t s) {
+  if (wtype == PE_W_BF16) {
+    if (op == DENSE_GLU) launch_sized<DENSE_GLU, PE_W_BF16>(a, s);
+    else launch_sized<DENSE_LINEAR, PE_W_BF16>(a, s);
+  } else if (wtype == PE_W_INT4_G128) {
+    if (op == DENSE_GLU) launch_sized<DENSE_GLU, PE_W_INT4_G128>(a, s);
+    else launch_sized<DENSE_LINEAR, PE_W_INT4_G128>(a, s);
+  } else {
+    if (op == DENSE_GLU) launch_sized<DENSE_GLU, PE_W_MXFP4_B32>(a, s);
+    else launch_sized<DENSE_LINEAR, PE_W_MXFP4_B32>(a, s);
+  }
+}
+
+void launch_grouped_back(DenseOp op, const GroupedArgs& a, hipStream_t s) {
+  if (op == DENSE_DGLU) launch_rows<DENSE_DGLU, false, 2, 2, 4, 4, 2>(a, s);
+  else launch_rows<DENSE_LINEAR, false, 2, 2, 4, 4, 2>(a, s);
+}
+
+void launch_grouped_weights(const GroupedArgs& a, hipStream_t s) {
+  constexpr int BT = 128, BN = 128, NST = 2;
+  const int64_t tiles = (int64_t)a.E * ((a.d.T + BT - 1) / BT) * ((a.d.N + BN - 1) / BN);
+  constexpr int kLds = std::max(NST * (BT + BN) * 128 + 32 * 64 * 4, BT * (BN + 4) * 4);
+  if (a.rows) grouped_weights_kernel<true, 2, 2, 4, 4, NST><<<dim3((unsigned)tiles), 256, kLds, s>>>(a);
+  else grouped_weights_kernel<false, 2, 2, 4, 4, NST><<<dim3((unsigned)tiles), 256, kLds, s>>>(a);
+}
+
+}  // namespace pe

@@ -411,6 +411,105 @@ int pe_ffn_backward(int device, int act, const void* dy, int64_t lddy, const voi
                     const void* w13, const void* w2, int T, int hidden, int inter, void* dgu, void* h, void* dx,
                     int64_t lddx, void* dw13, void* dw2, void* stream);
 
+/* ---- 4-bit products, and products grouped by expert -------------------------
+ *
+ * For experts that all stay in GPU memory, for training them, and for a shared
+ * expert or dense layer with 4-bit weights: pe_route's ids are put in the order
+ * of their experts, each expert multiplies its own rows, and the rows are summed
+ * back to tokens.  The conventions are those of the dense operators above: no
+ * context, no allocation, no state between calls, capturable, the same rules of
+ * alignment, strides and overlap.
+ *
+ * Weights, where bf16 is not the only type:
+ *   PE_W_BF16:      bf16 rows of K, K a multiple of 8; scales NULL.
+ *   PE_W_INT4_G128: as pe_load_expert takes them: u8 rows of K/2, fp16 scales,
+ *                   rows of K/128; K a multiple of 128.
+ *   PE_W_MXFP4_B32: u8 rows of K/2, E8M0 scale bytes, rows of K/32; K a multiple
+ *                   of 32.  A weight beyond bf16's range is infinite (scale
+ *                   bytes from 253 on make them); byte 255 makes its 32
+ *                   weights NaN.
+ * Weights and scales are contiguous, those of E experts one after another.
+ * x is bf16.  Sums are fp32.  int4 sums x (q - 8) as sum x q - 8 sum x, so their
+ * error is that of terms |x| (q + 8) s; where x holds an infinity, or values
+ * whose sum of 15 |x| passes fp32's range, the row's results are NaN or infinite.
+ *
+ * Rows grouped by expert: rows offsets[e] .. offsets[e+1] - 1 of a matrix of R
+ * rows belong to expert e (offsets int32 [E + 1] on the device, ascending from 0
+ * to at most R; an expert may have none).  Rows from offsets[E] on take part in
+ * nothing, and outputs leave theirs as they were.  `rows` int32 [R] gives the row
+ * of x (of x_rows) that each takes; with NULL that is its own, and x has R rows.
+ * Offsets and rows are read on the device and cannot be checked here: ones that
+ * break these rules give wrong results, but no access outside the buffers.
+ * num_experts <= 1024. */
+
+/* y[t,n] = act(sum_k x[t,k] w[n,k] + bias[n]) + residual[t,n], rounded once:
+ * pe_linear for w u8 [N, K/2] in PE_W_INT4_G128 or PE_W_MXFP4_B32. */
+int pe_linear_w4(int device, int wtype, const void* x, int64_t ldx, const void* w, const void* wscale,
+                 const void* bias, int act, const void* residual, int64_t ldr, int T, int N, int K, void* y,
+                 int64_t ldy, int ytype, void* stream);
+
+/* h[t,i] = act(g[t,i]) * u[t,i] with g = x W1^T, u = x W3^T: pe_glu for w13 u8
+ * [2*inter, hidden/2]; h bf16 [T, inter], inter a multiple of 8. */
+int pe_glu_w4(int device, int wtype, int act, const void* x, int64_t ldx, const void* w13, const void* s13, int T,
+              int hidden, int inter, void* h, int64_t ldh, void* stream);
+
+/* The routed entries of topk_ids int32 [T, top_k] (entry t*top_k + j) in the order
+ * of their experts, those of one expert in their own: offsets [E + 1] as above,
+ * rows [T*top_k] the token t of each place, places [T, top_k] the place each entry
+ * went to, -1 where its id is outside [0, E) (such entries have no place, and
+ * rows[offsets[E]] .. are left as they were).  T = 0 sets the offsets to zero.
+ * T * top_k is below 2^24; 4-byte alignment. */
+int pe_group_rows(int device, const int32_t* topk_ids, int T, int top_k, int num_experts, int32_t* offsets,
+                  int32_t* rows, int32_t* places, void* stream);
+
+/* y[p,n] = act(sum_k x[rows[p],k] w[e,n,k] + bias[e,n]) for the rows p of each
+ * expert e: w [E, N, K], bias bf16 [E, N] or NULL, y bf16 or fp32 [R, N] (ytype). */
+int pe_grouped_linear(int device, int wtype, const void* x, int64_t ldx, int x_rows, const int32_t* rows,
+                      const int32_t* offsets, const void* w, const void* wscale, const void* bias, int act, int R,
+                      int num_experts, int N, int K, void* y, int64_t ldy, int ytype, void* stream);
+
+/* h[p,i] = act(g[p,i]) * u[p,i] with g, u = x[rows[p]] w13[e]^T: w13 [E, 2*inter,
+ * hidden], h bf16 [R, inter], inter a multiple of 8; gu bf16 [R, 2*inter] or NULL:
+ * g and u, kept for pe_grouped_ffn_backward. */
+int pe_grouped_glu(int device, int wtype, int act, const void* x, int64_t ldx, int x_rows, const int32_t* rows,
+                   const int32_t* offsets, const void* w13, const void* s13, int R, int num_experts, int hidden,
+                   int inter, void* h, int64_t ldh, void* gu, void* stream);
+
+/* out[t] = sum_j topk_w[t,j] y[places[t,j]] + residual[t], in fp32 and in the
+ * order of j, rounded once: y bf16 [R, H], places int32 [T, top_k], topk_w fp32 [T,
+ * top_k] or NULL (1), residual bf16 [T, H] or NULL, out bf16 [T, H]; H a multiple
+ * of 8.  A place outside [0, R) adds nothing.  out may be the residual itself. */
+int pe_combine(int device, const void* y, int64_t ldy, int R, const int32_t* places, const float* topk_w,
+               const void* residual, int64_t ldr, int T, int top_k, int H, void* out, int64_t ldo, void* stream);
+
+/* Gradients of pe_combine for dout bf16 [T, H]: dy[places[t,j]] = topk_w[t,j]
+ * dout[t] (bf16 [R, H]; rows that no place names are left as they were) and
+ * dtopk_w[t,j] = sum_h dout[t,h] y[places[t,j],h] (fp32 [T, top_k]; 0 for a place
+ * outside [0, R)); either may be NULL, y may be without dtopk_w.  Two entries
+ * must not have the same place if dy is asked for.  The residual's gradient is
+ * dout.  T * top_k is below 2^26. */
+int pe_combine_backward(int device, const void* dout, int64_t lddo, const int32_t* places, const float* topk_w,
+                        const void* y, int64_t ldy, int R, int T, int top_k, int H, void* dy, int64_t lddy,
+                        float* dtopk_w, void* stream);
+
+/* Gradients of y[p] = h[p] W2[e]^T (h of pe_grouped_glu, bf16 weights, gu kept)
+ * for dy bf16 [R, hidden], the rows p of each expert e:
+ *   dh = dy W2[e];  dg = dh * u * act'(g);  du = dh * act(g);
+ *   dx[p] = dg W1[e] + du W3[e] [R, hidden] (a row for each p: pe_combine without
+ *   weights adds up those of a token);
+ *   dw13[e] = sum_p [dg, du][p]^T x[rows[p]] [E, 2*inter, hidden];
+ *   dw2[e] = sum_p dy[p]^T h[p] [E, hidden, inter], zeros for an expert without
+ *   rows; all bf16, each skipped if NULL (not all).
+ * dgu bf16 [R, 2*inter] receives dg and du, and h bf16 [R, inter] (with dw2 only;
+ * NULL otherwise) is made again from gu; both are read back as bf16, which makes
+ * the gradients' error about 1.4 times that of one rounding.  w2 bf16 [E, hidden,
+ * inter].  hidden and inter are multiples of 8.  x may be NULL without dw13, w13
+ * without dx.  R = 0 sets dw13 and dw2 to zero. */
+int pe_grouped_ffn_backward(int device, int act, const void* dy, int64_t lddy, const void* x, int64_t ldx, int x_rows,
+                            const int32_t* rows, const int32_t* offsets, const void* gu, const void* w13,
+                            const void* w2, int R, int num_experts, int hidden, int inter, void* dgu, void* h,
+                            void* dx, int64_t lddx, void* dw13, void* dw2, void* stream);
+
 const char* pe_strerror(int status);
 const char* pe_last_error(void);
 

@@ -4,81 +4,126 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/pe.h"
 #include "pe_dense.h"
 #include "pe_grouped.h"
+#include "pe_layout.h"
 #include "pe_tiles.h"
 
 namespace pe {
 
 // ------------------------------------------------------------------ order by expert
 //
-// A stable counting sort of the routed ids without scratch memory: the workgroup
-// of expert e counts the ids below e (its first place) and those equal to e, each
-// wavefront over its own stretch of ids, and then numbers the latter in order
-// with ballots.  Every workgroup reads all ids, from L2 after the first.
-template <int NW>
+// A stable counting sort of the routed ids without scratch memory: every workgroup counts all ids by expert, those before
+// its own 64 NW PER apart, and so knows where its entries go without the others.  Among its own, a wavefront's come in
+// the order of its lanes (those of one expert find each other by a ballot for each bit of the id), wavefronts' in
+// theirs.  8192 x 8 ids, 128 experts: 8 us, a tenth of it for the bytes.  (A workgroup for each expert that numbers its
+// entries took 24: entries of one expert lie far apart, and each was a store of its own to lines that others write.)
+template <int NW, int PER>
 __global__ __launch_bounds__(NW * 64) void group_rows_kernel(GroupRowsArgs a) {
-  __shared__ int eq_of[NW], lt_of[NW];
-  const int e = blockIdx.x, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int stretch = ((a.n + NW - 1) / NW + 63) / 64 * 64;
-  const int from = wave * stretch, to = min(from + stretch, a.n);
-  int eq = 0, lt = 0;
-#pragma unroll 4
-  for (int i = from + lane; i < to; i += 64) {
-    const uint32_t id = (uint32_t)a.ids[i];           // ids below 0 are above every expert
-    eq += id == (uint32_t)e;
-    lt += id < (uint32_t)e;
+  constexpr int kThreads = NW * 64, kOwn = kThreads * PER, kBatch = 8;
+  __shared__ int before[kMaxExperts], rest[kMaxExperts], sums[NW];
+  __shared__ uint16_t counts[NW][kMaxExperts];           // of the wavefronts' own entries, 64 PER at most
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, own = blockIdx.x * kOwn;
+  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    before[e] = rest[e] = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) counts[w][e] = 0;
   }
-  auto add = [](int p, int q) { return p + q; };
-  eq = group_reduce<64>(eq, add);
-  lt = group_reduce<64>(lt, add);
-  int base = 0, count = 0;
-  if constexpr (NW > 1) {
-    if (lane == 0) {
-      eq_of[wave] = eq;
-      lt_of[wave] = lt;
-    }
-    __syncthreads();
+  __syncthreads();
+  for (int i0 = threadIdx.x; i0 < a.n; i0 += kThreads * kBatch) {
+    uint32_t id[kBatch];
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      base += lt_of[w] + (w < wave ? eq_of[w] : 0);
-      count += eq_of[w];
-    }
-    if (threadIdx.x == 0) {
-      int first = 0;
+    for (int j = 0; j < kBatch; ++j) id[j] = (uint32_t)a.ids[min(i0 + j * kThreads, a.n - 1)];
 #pragma unroll
-      for (int w = 0; w < NW; ++w) first += lt_of[w];
-      a.offsets[e] = first;
-      if (e == a.E - 1) a.offsets[a.E] = first + count;
-    }
-  } else {
-    base = lt;
-    if (threadIdx.x == 0) {
-      a.offsets[e] = lt;
-      if (e == a.E - 1) a.offsets[a.E] = lt + eq;
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + j * kThreads;
+      if (i < a.n && id[j] < (uint32_t)a.E) atomicAdd(i < own ? &before[id[j]] : &rest[id[j]], 1);   // counts: in any order
     }
   }
-  for (int i0 = from; i0 < to; i0 += 64) {
-    const int i = i0 + lane;
-    const int id = i < to ? a.ids[i] : e ? -1 : a.E;
-    const bool mine = i < to && id == e;
-    const uint64_t m = __ballot(mine);
-    if (mine) {
-      const int p = base + __popcll(m & ((1ull << lane) - 1));
+  // own entries: a wavefront's are 64 PER in a row.  `place` is first the place among the wavefront's of that expert
+  int id[PER], place[PER];
+  const int bits = 32 - __clz(a.E);
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int i = own + wave * 64 * PER + 64 * j + lane;
+    id[j] = i < a.n ? a.ids[i] : -1;
+    const bool in = (uint32_t)id[j] < (uint32_t)a.E;
+    uint64_t same = __ballot(in);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t set = __ballot(id[j] >> b & 1);
+      same &= id[j] >> b & 1 ? set : ~set;
+    }
+    place[j] = -1;
+    if (in) {
+      const int rank = __popcll(same & ((1ull << lane) - 1));
+      place[j] = counts[wave][id[j]] + rank;
+    }
+    __builtin_amdgcn_wave_barrier();                     // all lanes have read before one of an expert's adds theirs
+    if (in && (same & ((1ull << lane) - 1)) == 0) counts[wave][id[j]] += (uint16_t)__popcll(same);
+    __builtin_amdgcn_wave_barrier();
+  }
+  __syncthreads();
+  // offsets: a prefix sum over the experts, E / (64 NW) of them a thread
+  constexpr int kEach = (kMaxExperts + kThreads - 1) / kThreads;
+  int all[kEach], total = 0;
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    const int e = threadIdx.x * kEach + j;
+    all[j] = e < a.E ? before[e] + rest[e] : 0;
+    total += all[j];
+  }
+  int upto = total;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(upto, d);
+    if (lane >= d) upto += v;
+  }
+  if (lane == 63) sums[wave] = upto;
+  __syncthreads();
+  int first = upto - total;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) first += w < wave ? sums[w] : 0;
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    const int e = threadIdx.x * kEach + j;
+    if (e < a.E) {
+      before[e] += first;                                // place of the workgroup's first entry of the expert
+      if (blockIdx.x == 0) {
+        a.offsets[e] = first;
+        if (e == a.E - 1) a.offsets[a.E] = first + all[j];
+      }
+    }
+    first += all[j];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int i = own + wave * 64 * PER + 64 * j + lane;
+    if (place[j] >= 0) {
+      int p = before[id[j]] + place[j];
+#pragma unroll
+      for (int w = 0; w < NW - 1; ++w) p += w < wave ? counts[w][id[j]] : 0;
       a.rows[p] = i / a.k;
       a.places[i] = p;
+    } else if (i < a.n) {
+      a.places[i] = -1;
     }
-    if (e == 0 && i < to && (uint32_t)id >= (uint32_t)a.E) a.places[i] = -1;
-    base += __popcll(m);
   }
 }
 
+template <int NW, int PER>
+static void launch_group_rows_n(const GroupRowsArgs& a, hipStream_t s) {
+  constexpr int kOwn = NW * 64 * PER;
+  group_rows_kernel<NW, PER><<<dim3(std::max(1, (a.n + kOwn - 1) / kOwn)), NW * 64, 0, s>>>(a);
+}
+
 void launch_group_rows(const GroupRowsArgs& a, hipStream_t s) {
-  if (a.n <= 512) group_rows_kernel<1><<<dim3(a.E), 64, 0, s>>>(a);
-  else if (a.n <= 4096) group_rows_kernel<4><<<dim3(a.E), 256, 0, s>>>(a);
-  else group_rows_kernel<16><<<dim3(a.E), 1024, 0, s>>>(a);
+  if (a.n <= 1024) launch_group_rows_n<4, 4>(a, s);
+  else if (a.n <= 131072) launch_group_rows_n<16, 1>(a, s);
+  else launch_group_rows_n<16, 8>(a, s);
 }
 
 // ------------------------------------------------------------------ sum back to tokens
@@ -191,35 +236,33 @@ struct Tile {
   int col;        // tile of columns
 };
 
-// The tile of block `b` among nn tiles of columns; false if there is none.  XCD: neighbouring tiles go to one XCD, an
-// expert's in bands of 8 tiles of rows, column by column (as tile_of does for one matrix).
-template <int BT, bool XCD>
-__device__ __forceinline__ bool find_tile(const GroupedArgs& a, int b, int nn, Tile& t) {
-  constexpr int kBand = 8, kPer = 16;                    // at most 1024 experts
-  if (!a.offsets) {
-    const int nt = (a.R + BT - 1) / BT;
-    int tt = b, tn = 0;
-    if constexpr (XCD) tile_of(b, nt, nn, tt, tn);
-    t = Tile{0, tt * BT, a.R, tn};
-    return true;
-  }
+// Sum of the values of all lanes up to and with this one.
+__device__ __forceinline__ int prefix_sum(int v) {
+  auto add = [&](auto ctrl, auto rows) {
+    v += __builtin_amdgcn_update_dpp(0, v, decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
+  };
+  using std::integral_constant;
+  add(integral_constant<int, 0x111>{}, integral_constant<int, 0xF>{});    // from 1, 2, 4 and 8 lanes before, in each 16
+  add(integral_constant<int, 0x112>{}, integral_constant<int, 0xF>{});
+  add(integral_constant<int, 0x114>{}, integral_constant<int, 0xF>{});
+  add(integral_constant<int, 0x118>{}, integral_constant<int, 0xF>{});
+  add(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});    // lane 15 to the second 16, 47 to the fourth
+  add(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});    // lane 31 to the upper half
+  return v;
+}
+
+// find_tile for E / 64 (rounded up) <= PER experts a lane
+template <int BT, bool XCD, int PER>
+__device__ __forceinline__ bool find_expert_tile(const GroupedArgs& a, int b, int nn, Tile& t) {
+  constexpr int kBand = 8;
   const int lane = threadIdx.x & 63, per = (a.E + 63) / 64;
-  int o[kPer + 1];
+  int o[PER + 1];
 #pragma unroll
-  for (int i = 0; i <= kPer; ++i) {
-    o[i] = 0;
-    if (i <= per) o[i] = min(max(a.offsets[min(lane * per + i, a.E)], 0), a.R);
-  }
+  for (int i = 0; i <= PER; ++i) o[i] = min(max(a.offsets[min(lane * per + min(i, per), a.E)], 0), a.R);
   int mine = 0;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    if (i < per) mine += (max(o[i + 1] - o[i], 0) + BT - 1) / BT;
-  int upto = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(upto, d);
-    if (lane >= d) upto += v;
-  }
+  for (int i = 0; i < PER; ++i) mine += (max(o[i + 1] - o[i], 0) + BT - 1) / BT;
+  const int upto = prefix_sum(mine);
   const int total = __builtin_amdgcn_readlane(upto, 63) * nn;
   if (b >= total) return false;
   int q = b;
@@ -228,13 +271,13 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& a, int b, int nn, T
     const int xcd = b % kXcds;
     q = xcd * (total / kXcds) + min(xcd, total % kXcds) + b / kXcds;
   }
-  const int at = q / nn;                                 // row tile, were the columns the faster index
+  const int at = XCD ? q / nn : q;                       // row tile, were the columns the faster index
   const int owner = __popcll(__ballot(upto <= at));
   int before = __builtin_amdgcn_readlane(upto - mine, owner), e = owner * per, lo = 0, hi = 0, tiles = 0;
   bool found = false;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (i < per && !found) {
+  for (int i = 0; i < PER; ++i) {
+    if (!found) {
       lo = __builtin_amdgcn_readlane(o[i], owner);
       hi = __builtin_amdgcn_readlane(o[i + 1], owner);
       tiles = (max(hi - lo, 0) + BT - 1) / BT;
@@ -245,10 +288,29 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& a, int b, int nn, T
       }
     }
   }
-  const int r = q - before * nn;                         // among the expert's own
-  const int band = r / (kBand * nn), rows = min(kBand, tiles - band * kBand), in = r - band * kBand * nn;
-  t = Tile{e, lo + (band * kBand + in % rows) * BT, hi, in / rows};
+  if constexpr (XCD) {
+    const int r = q - before * nn;                       // among the expert's own
+    const int band = r / (kBand * nn), rows = min(kBand, tiles - band * kBand), in = r - band * kBand * nn;
+    t = Tile{e, lo + (band * kBand + in % rows) * BT, hi, in / rows};
+  } else {
+    t = Tile{e, lo + (at - before) * BT, hi, 0};
+  }
   return true;
+}
+
+// The tile of block `b` among nn tiles of columns; false if there is none.  XCD: neighbouring tiles go to one XCD, an
+// expert's in bands of 8 tiles of rows, column by column (as tile_of does for one matrix).  Otherwise nn is 1.
+template <int BT, bool XCD>
+__device__ __forceinline__ bool find_tile(const GroupedArgs& a, int b, int nn, Tile& t) {
+  if (!a.offsets) {
+    const int nt = (a.R + BT - 1) / BT;
+    int tt = b, tn = 0;
+    if constexpr (XCD) tile_of(b, nt, nn, tt, tn);
+    t = Tile{0, tt * BT, a.R, tn};
+    return true;
+  }
+  if (a.E <= 128) return find_expert_tile<BT, XCD, 2>(a, b, nn, t);
+  return find_expert_tile<BT, XCD, kMaxExperts / 64>(a, b, nn, t);
 }
 
 // The row of x that row p of the output takes.
@@ -413,12 +475,12 @@ __global__ __launch_bounds__(WT * WN * 64) void grouped_weights_kernel(GroupedAr
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wt = wave / WN, wn = wave % WN;
   const int nt = (g.d.T + BT - 1) / BT, nn = (g.d.N + BN - 1) / BN;
-  // neighbouring tiles on one XCD, an expert's all together
-  const int total = g.E * nt * nn, xcd = blockIdx.x % 8;
-  const int q = xcd * (total / 8) + min(xcd, total % 8) + blockIdx.x / 8;
-  const int e = q / (nt * nn), in = q - e * nt * nn;
-  const int band = in / (8 * nn), brows = min(8, nt - band * 8), r = in - band * 8 * nn;
-  const int t0 = (band * 8 + r % brows) * BT, n0 = r / brows * BN;
+  // Each XCD takes an eighth of every expert's tiles, column by column: an expert's whole on one XCD would leave
+  // the XCDs as uneven as the experts.
+  const int share = (nt * nn + 7) / 8, turn = blockIdx.x / 8;
+  const int e = turn / share, in = blockIdx.x % 8 * share + turn % share;
+  if (in >= nt * nn) return;
+  const int t0 = in % nt * BT, n0 = in / nt * BN;
   const int r0 = min(max(g.offsets[e], 0), g.R), r1 = min(max(g.offsets[e + 1], 0), g.R);
   DenseArgs a = g.d;
   a.y = static_cast<uint16_t*>(a.y) + (int64_t)e * a.T * a.N;
@@ -499,7 +561,28 @@ __global__ __launch_bounds__(WT * WN * 64) void grouped_weights_kernel(GroupedAr
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j], af[i], acc[i][j], 0, 0, 0);
     }
   }
-  finish_tile<DENSE_LINEAR, WT, WN, FT, FN>(a, lds, t0, n0, acc);
+  // As finish_tile; the gradients are stored past the caches, which the rows of the tiles after them would lose otherwise
+  // (dw13 of 128 experts of 128 rows, 1536 x 2048: 373 us through them, 289 past them).
+  constexpr int LR = BN + 4, kChunks = BN / 8;
+  float* tile = reinterpret_cast<float*>(lds);
+  wait_stage<0>();
+#pragma unroll
+  for (int i = 0; i < FT; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      *reinterpret_cast<f32x4_t*>(tile + ((wt * FT + i) * 16 + (lane & 15)) * LR + (wn * FN + j) * 16 + (lane >> 4) * 4) =
+          acc[i][j];
+  __syncthreads();
+#pragma unroll 1
+  for (int idx = threadIdx.x; idx < BT * kChunks; idx += NW * 64) {
+    const int m = idx / kChunks, c = (idx % kChunks) * 8;
+    if (t0 + m >= a.T || n0 + c >= a.N) continue;        // (N is a multiple of 8)
+    const float4 lo = *reinterpret_cast<const float4*>(tile + m * LR + c), hi = *reinterpret_cast<const float4*>(tile + m * LR + c + 4);
+    const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, narrow8(v)),
+                                reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.y) + (int64_t)(t0 + m) * a.N + n0 + c));
+  }
 }
 
 // ------------------------------------------------------------------ 4-bit weights
@@ -558,135 +641,172 @@ __device__ __forceinline__ float half_value(uint16_t h) { return (float)__builti
 // ------------------------------------------------------------------ products of few rows
 //
 // A few rows for each matrix (a decode step): the weights' bytes bound the product, so they stream straight from memory
-// into MFMA operands.  A workgroup takes 16 / P weight rows (of a GLU 16 / P gate rows and their up rows) and 16 / P
-// rows of x, its KW wavefronts every KW-th step of k each with U steps in flight; the partial sums meet in LDS in a
-// fixed order.  A step is 128 bytes of k in bf16 and 64 bytes, 128 k, in 4 bits: a lane's 16 bytes of codes are
-// 32 consecutive k, one MXFP4 block.  P parts of k share the MFMA's 16 x 16 block as in the dense kernel of few rows.
-// x is the first operand, so that a lane's accumulators belong to one weight row and its scale.
-template <DenseOp OP, int WTYPE, int KW, int P, int U>
-__global__ __launch_bounds__(KW * 64) void grouped_few_kernel(GroupedArgs g) {
-  constexpr int NR = 16 / P, F = OP == DENSE_GLU ? 2 : 1;
+// into MFMA operands.  A wavefront takes F fragments of 16 / P weight rows (of a GLU gate rows and their up rows)
+// and 16 / P rows of x, every KW-th step of k with U steps in flight; CW wavefronts take neighbouring columns, KW share
+// their sums, which meet in LDS in a fixed order.  A step is 128 bytes of k in bf16 and 64 bytes, 128 k, in 4 bits.  P
+// parts of k share the MFMA's 16 x 16 block as in the dense kernel of few rows.  x is the first operand, so that a lane's
+// accumulators belong to one weight row and its scale.
+template <DenseOp OP, int WTYPE, int F, int CW, int KW, int P, int U>
+__global__ __launch_bounds__(CW * KW * 64) void grouped_few_kernel(GroupedArgs g) {
+  static_assert(OP != DENSE_GLU || F == 2, "a gate and an up fragment");
+  constexpr int NR = 16 / P, FO = OP == DENSE_GLU ? 1 : F, NO = CW * FO * NR;
+  constexpr int WM = OP == DENSE_GLU ? 2 : 1;            // matrices of N rows
   constexpr bool Q = WTYPE != PE_W_BF16;
   constexpr int kStep = Q ? 128 : 64, kX = Q ? 4 : 2, kW = Q ? 1 : 2;
-  __shared__ f32x4_t red[F][KW][64];
+  __shared__ f32x4_t red[CW][F][KW][64];
   Tile tile;
   if (!find_tile<NR, false>(g, blockIdx.y, 1, tile)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int cw = wave / KW, kw = wave % KW;
   const int q = lane >> 4, ln = lane & 15, part = ln / NR, lr = ln % NR;
-  const int K = g.d.K, N = g.d.N;
+  const int K = g.d.K, N = g.d.N, t0 = tile.t0;
   const int64_t row_bytes = Q ? K / 2 : (int64_t)K * 2;
-  const DenseArgs a = expert_args(g, tile.e, tile.t1, F * N * row_bytes);
-  const int n0 = blockIdx.x * NR, t0 = tile.t0;
-  const int nk = (K + kStep - 1) / kStep;
-  const int wrow = min(n0 + lr, N - 1);
-  const char* px = static_cast<const char*>(a.a) + x_row(g, min(t0 + lr, a.T - 1)) * a.lda * 2;
+  const DenseArgs a = expert_args(g, tile.e, tile.t1, WM * N * row_bytes);
+  const int64_t row = x_row(g, min(t0 + lr, a.T - 1));
+  const int n0 = blockIdx.x * NO, nk = (K + kStep - 1) / kStep;
+  // each fragment's first weight row, and this lane's from there: at most 16 rows of 2^23 bytes
   const char* pw[F];
-  const uint16_t* s16[F];
-  const uint8_t* s8[F];
+  const char* ps[F];
+  uint32_t ow[F], os[F];
 #pragma unroll
   for (int f = 0; f < F; ++f) {
-    pw[f] = static_cast<const char*>(a.b) + ((int64_t)f * N + wrow) * row_bytes + 16 * q;
-    const int64_t at = ((int64_t)tile.e * F * N + (int64_t)f * N + wrow) * (K / kScaleGroup<WTYPE>);
-    s16[f] = static_cast<const uint16_t*>(g.ws) + at;
-    s8[f] = static_cast<const uint8_t*>(g.ws) + at;
+    const int first = min(n0 + (OP == DENSE_GLU ? cw : cw * F + f) * NR, N - 1), mine = min(lr, N - 1 - first);
+    const int64_t at = first + (OP == DENSE_GLU && f ? (int64_t)N : 0);
+    const uint32_t scales = K / kScaleGroup<WTYPE> * (kInt4<WTYPE> ? 2 : 1);     // bytes of a row's
+    pw[f] = static_cast<const char*>(a.b) + at * row_bytes;
+    ps[f] = static_cast<const char*>(g.ws) + ((int64_t)tile.e * WM * N + at) * scales;
+    ow[f] = mine * (uint32_t)row_bytes;
+    os[f] = mine * scales;
   }
   f32x4_t acc[F];
 #pragma unroll
   for (int f = 0; f < F; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int k0 = wave * P; k0 < nk; k0 += KW * P * U) {
+  // U steps from k0 on.  Where not all of them are `whole`, loads beyond the end take the row's last bytes instead and
+  // their operands are set to zero: loads under conditions would be issued one after another.
+  auto steps = [&](int k0, auto whole_t) {
+    constexpr bool whole = decltype(whole_t)::value;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
     uint4 w[U][F][kW], x[U][kX];
-    float s[U][F];
+    uint32_t s[U][F];
+    const char* px = static_cast<const char*>(a.a) + row * a.lda * 2;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = k0 + u * KW * P + part;
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      if constexpr (Q) {
-        const bool in = k * 128 + 32 * q < K;
+      const int blk = whole ? 4 * k + q : min(4 * k + q, K / 32 - 1);         // 4 bits: this lane's 32 k
 #pragma unroll
-        for (int f = 0; f < F; ++f) {
-          w[u][f][0] = in ? *reinterpret_cast<const uint4*>(pw[f] + (int64_t)k * 64) : zero;
-          s[u][f] = 0.f;
-          if (in) s[u][f] = kInt4<WTYPE> ? half_value(s16[f][k]) : e8m0(s8[f][4 * k + q]);
-        }
+      for (int f = 0; f < F; ++f) {
+        if constexpr (Q) {
+          w[u][f][0] = *reinterpret_cast<const uint4*>(pw[f] + (ow[f] + blk * 16u));
+          if constexpr (kInt4<WTYPE>) s[u][f] = *reinterpret_cast<const uint16_t*>(ps[f] + (os[f] + (blk / 4) * 2u));
+          else s[u][f] = *reinterpret_cast<const uint8_t*>(ps[f] + (os[f] + blk));
+        } else {
 #pragma unroll
-        for (int c = 0; c < kX; ++c)
-          x[u][c] = in ? *reinterpret_cast<const uint4*>(px + (int64_t)k * 256 + 64 * q + 16 * c) : zero;
-      } else {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const bool in = k * 64 + 32 * c + 8 * q < K;
-#pragma unroll
-          for (int f = 0; f < F; ++f)
-            w[u][f][c] = in ? *reinterpret_cast<const uint4*>(pw[f] + (int64_t)k * 128 + 64 * c) : zero;
-          x[u][c] = in ? *reinterpret_cast<const uint4*>(px + (int64_t)k * 128 + 64 * c + 16 * q) : zero;
+          for (int c = 0; c < 2; ++c) {
+            const int at = k * 64 + 32 * c + 8 * q;
+            w[u][f][c] = *reinterpret_cast<const uint4*>(pw[f] + (ow[f] + (whole ? at : min(at, K - 8)) * 2u));
+          }
         }
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * KW * P + part;
+#pragma unroll
+      for (int c = 0; c < kX; ++c) {
+        if constexpr (Q) {
+          const int blk = whole ? 4 * k + q : min(4 * k + q, K / 32 - 1);
+          x[u][c] = *reinterpret_cast<const uint4*>(px + (int64_t)blk * 64 + 16 * c);
+        } else {
+          const int at = k * 64 + 32 * c + 8 * q;
+          x[u][c] = *reinterpret_cast<const uint4*>(px + (int64_t)(whole ? at : min(at, K - 8)) * 2);
+        }
+      }
+    }
+    if constexpr (!whole) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int c = 0; c < kX; ++c) {
+          const int k = k0 + u * KW * P + part;
+          if ((Q ? 128 * k + 32 * q : k * 64 + 32 * c + 8 * q) < K) continue;
+          x[u][c] = zero;
+#pragma unroll
+          for (int f = 0; f < F; ++f) {
+            w[u][f][Q ? 0 : c] = zero;
+            s[u][f] = kMx<WTYPE> ? 127 : 0;
+          }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      f32x4_t start = f32x4_t{0.f, 0.f, 0.f, 0.f};
       if constexpr (kInt4<WTYPE>) {
-        f32x4_t start = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           start = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x[u][c]), minus8(), start, 0, 0, 0);
+      }
 #pragma unroll
-        for (int f = 0; f < F; ++f) {
-          const uint32_t d[4] = {w[u][f][0].x, w[u][f][0].y, w[u][f][0].z, w[u][f][0].w};
-          f32x4_t p = start;
+      for (int f = 0; f < F; ++f) {
+        f32x4_t p = kInt4<WTYPE> ? start : acc[f];
+        const float scale = kMx<WTYPE> ? e8m0(s[u][f]) : 0.f;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x[u][c]), decode8<WTYPE>(d[c], 0.f), p,
-                                                        0, 0, 0);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[f][i] = __builtin_fmaf(p[i], s[u][f], acc[f][i]);
-        }
-      } else {
-#pragma unroll
-        for (int f = 0; f < F; ++f)
-#pragma unroll
-          for (int c = 0; c < kX; ++c) {
-            bf16x8_t v;
-            if constexpr (Q) {
-              const uint32_t d[4] = {w[u][f][0].x, w[u][f][0].y, w[u][f][0].z, w[u][f][0].w};
-              v = decode8<WTYPE>(d[c], s[u][f]);
-            } else {
-              v = __builtin_bit_cast(bf16x8_t, w[u][f][c]);
-            }
-            acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x[u][c]), v, acc[f], 0, 0, 0);
+        for (int c = 0; c < kX; ++c) {
+          bf16x8_t v;
+          if constexpr (Q) {
+            const uint32_t d[4] = {w[u][f][0].x, w[u][f][0].y, w[u][f][0].z, w[u][f][0].w};
+            v = decode8<WTYPE>(d[c], scale);
+          } else {
+            v = __builtin_bit_cast(bf16x8_t, w[u][f][c]);
           }
+          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x[u][c]), v, p, 0, 0, 0);
+        }
+        if constexpr (kInt4<WTYPE>) {
+          const float by = half_value((uint16_t)s[u][f]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[f][i] = __builtin_fmaf(p[i], by, acc[f][i]);
+        } else {
+          acc[f] = p;
+        }
       }
     }
-  }
+  };
+  const int full = K / kStep;                            // steps of which everything exists
+  int k0 = kw * P;
+  for (; k0 + (U - 1) * KW * P + P <= full; k0 += KW * P * U) steps(k0, std::true_type{});
+  for (; k0 < nk; k0 += KW * P * U) steps(k0, std::false_type{});
 #pragma unroll
-  for (int f = 0; f < F; ++f) red[f][wave][lane] = acc[f];
+  for (int f = 0; f < F; ++f) red[cw][f][kw][lane] = acc[f];
   __syncthreads();
 
-  // Four consecutive columns of one row per thread: their P parts of the KW sums.
-  if (threadIdx.x >= NR * NR / 4) return;
-  const int tr = threadIdx.x / (NR / 4), c4 = threadIdx.x % (NR / 4) * 4;
-  const int t = t0 + tr, n = n0 + c4;
-  if (t >= a.T || n >= N) return;
-  auto sum = [&](int f, float (&v)[4]) {
+  // Four consecutive columns of one row at a time: their P parts of the KW sums.
+  constexpr int kChunks = NO / 4;
+  for (int idx = threadIdx.x; idx < NR * kChunks; idx += CW * KW * 64) {
+    const int tr = idx / kChunks, c4 = idx % kChunks * 4;
+    const int t = t0 + tr, n = n0 + c4;
+    if (t >= a.T || n >= N) continue;
+    auto sum = [&](int group, int f, int c, float (&v)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = 0.f;
+      for (int i = 0; i < 4; ++i) {
+        v[i] = 0.f;
 #pragma unroll
-      for (int p = 0; p < P; ++p)
+        for (int p = 0; p < P; ++p)
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          const int row = p * NR + tr;
-          v[i] += reinterpret_cast<const float*>(&red[f][w][row / 4 * 16 + p * NR + c4 + i])[row % 4];
-        }
+          for (int w = 0; w < KW; ++w) {
+            const int r = p * NR + tr;
+            v[i] += reinterpret_cast<const float*>(&red[group][f][w][r / 4 * 16 + p * NR + c + i])[r % 4];
+          }
+      }
+    };
+    float v[4];
+    if constexpr (OP == DENSE_GLU) {
+      float u[4];
+      sum(c4 / NR, 0, c4 % NR, v);
+      sum(c4 / NR, 1, c4 % NR, u);
+      finish_glu(a, t, n, true, v, u);
+    } else {
+      sum(c4 / (F * NR), c4 / NR % F, c4 % NR, v);
+      finish_linear(a, t, n, v);
     }
-  };
-  float v[4];
-  sum(0, v);
-  if constexpr (OP == DENSE_GLU) {
-    float u[4];
-    sum(1, u);
-    finish_glu(a, t, n, true, v, u);
-  } else {
-    finish_linear(a, t, n, v);
   }
 }
 
@@ -882,22 +1002,32 @@ void launch_quant(const GroupedArgs& a, hipStream_t s) {
   quant_tile_kernel<OP, WTYPE, WT, WN, FT, FN, NST><<<dim3((unsigned)tiles), WT * WN * 64, kLds, s>>>(a);
 }
 
-template <DenseOp OP, int WTYPE, int KW, int P, int U>
+template <DenseOp OP, int WTYPE, int F, int CW, int KW, int P, int U>
 void launch_few(const GroupedArgs& a, hipStream_t s) {
-  constexpr int NR = 16 / P;
-  grouped_few_kernel<OP, WTYPE, KW, P, U>
-      <<<dim3((a.d.N + NR - 1) / NR, (unsigned)row_tiles(a, NR)), KW * 64, 0, s>>>(a);
+  constexpr int NR = 16 / P, NO = CW * NR * (OP == DENSE_GLU ? 1 : F);
+  grouped_few_kernel<OP, WTYPE, F, CW, KW, P, U>
+      <<<dim3((a.d.N + NO - 1) / NO, (unsigned)row_tiles(a, NR)), CW * KW * 64, 0, s>>>(a);
 }
 
 template <DenseOp OP, int WTYPE>
 void launch_sized(const GroupedArgs& a, hipStream_t s) {
   const int rows = a.offsets ? a.R / std::min(a.E, a.R) : a.R;    // of a matrix
-  if (rows <= 32 && row_tiles(a, 16) < 65536) {
-    launch_few<OP, WTYPE, 4, 1, 4>(a, s);
+  if (rows <= 32 && row_tiles(a, 8) < 65536) {
+    auto blocks = [&](int nr, int cols) { return row_tiles(a, nr) * ((a.d.N + cols - 1) / cols); };
+    if constexpr (OP == DENSE_GLU) {
+      if (rows > 8) launch_few<OP, WTYPE, 2, 1, 4, 1, 2>(a, s);
+      else if (WTYPE == PE_W_BF16 || blocks(8, 8) <= 1024) launch_few<OP, WTYPE, 2, 1, 4, 2, 2>(a, s);
+      else launch_few<OP, WTYPE, 2, 2, 2, 2, 2>(a, s);
+    } else {
+      if (a.d.K <= 1024) launch_few<OP, WTYPE, 2, 2, 2, 1, 3>(a, s);
+      else if (rows <= 8 && blocks(8, 8) <= 512) launch_few<OP, WTYPE, 1, 1, 4, 2, 2>(a, s);
+      else if (blocks(16, 32) >= 128) launch_few<OP, WTYPE, 2, 1, 4, 1, 2>(a, s);
+      else launch_few<OP, WTYPE, 2, 1, 4, 2, 2>(a, s);
+    }
     return;
   }
-  if constexpr (WTYPE == PE_W_BF16) launch_rows<OP, true, 2, 2, 4, 4, 2>(a, s);
-  else launch_quant<OP, WTYPE, 2, 2, 4, 4, 3>(a, s);
+  if constexpr (WTYPE == PE_W_BF16) launch_rows<OP, true, 2, 4, 4, 2, 2>(a, s);
+  else launch_quant<OP, WTYPE, 2, 4, 4, 2, 3>(a, s);
 }
 
 }  // namespace
@@ -916,16 +1046,27 @@ void launch_grouped(DenseOp op, int wtype, const GroupedArgs& a, hipStream_t s) 
 }
 
 void launch_grouped_back(DenseOp op, const GroupedArgs& a, hipStream_t s) {
-  if (op == DENSE_DGLU) launch_rows<DENSE_DGLU, false, 2, 2, 4, 4, 2>(a, s);
-  else launch_rows<DENSE_LINEAR, false, 2, 2, 4, 4, 2>(a, s);
+  if (op == DENSE_DGLU) launch_rows<DENSE_DGLU, false, 2, 4, 4, 2, 2>(a, s);
+  else launch_rows<DENSE_LINEAR, false, 2, 4, 4, 2, 2>(a, s);
 }
 
-void launch_grouped_weights(const GroupedArgs& a, hipStream_t s) {
-  constexpr int BT = 128, BN = 128, NST = 2;
-  const int64_t tiles = (int64_t)a.E * ((a.d.T + BT - 1) / BT) * ((a.d.N + BN - 1) / BN);
+namespace {
+
+template <bool GATHER, int WT, int WN, int FT, int FN, int NST>
+void launch_weights(const GroupedArgs& a, hipStream_t s) {
+  constexpr int BT = WT * FT * 16, BN = WN * FN * 16;
   constexpr int kLds = std::max(NST * (BT + BN) * 128 + 32 * 64 * 4, BT * (BN + 4) * 4);
-  if (a.rows) grouped_weights_kernel<true, 2, 2, 4, 4, NST><<<dim3((unsigned)tiles), 256, kLds, s>>>(a);
-  else grouped_weights_kernel<false, 2, 2, 4, 4, NST><<<dim3((unsigned)tiles), 256, kLds, s>>>(a);
+  static_assert(kLds <= 160 * 1024, "LDS of one workgroup");
+  const int64_t tiles = (int64_t)((a.d.T + BT - 1) / BT) * ((a.d.N + BN - 1) / BN);
+  grouped_weights_kernel<GATHER, WT, WN, FT, FN, NST>
+      <<<dim3((unsigned)((tiles + 7) / 8 * 8 * a.E)), WT * WN * 64, kLds, s>>>(a);
+}
+
+}  // namespace
+
+void launch_grouped_weights(const GroupedArgs& a, hipStream_t s) {
+  if (a.rows) launch_weights<true, 2, 4, 4, 2, 2>(a, s);
+  else launch_weights<false, 2, 4, 4, 2, 2>(a, s);
 }
 
 }  // namespace pe

@@ -336,15 +336,30 @@ struct RowOperand {
       at[i] = kMin == kPer || wave < kInstr ? row(r) + kc[i] : nullptr;
     }
   }
-  // Copy the 128 bytes at byte `from` of each row, of which the first `valid` exist.
-  __device__ __forceinline__ void copy(uint32_t lds, int wave, int64_t from, int valid) const {
+  // This wavefront's copies of a step where only the first `rows` rows exist.
+  static __device__ __forceinline__ int copies(int wave, int rows) {
+    return min(max((rows + 7) / 8 - wave + NW - 1, 0) / NW, kPer);
+  }
+  // Copy the 128 bytes at byte `from` of each row, of which the first `valid` exist, in this many copies.
+  __device__ __forceinline__ void copy(uint32_t lds, int wave, int64_t from, int valid, int n) const {
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (kMin == kPer || wave < kInstr)
+      if (i < n)
         copy_to_lds(lds + (wave + i * NW) * 1024,
                     valid == 128 || kc[i] < valid ? at[i] + from : reinterpret_cast<const char*>(g_zeros));
   }
 };
+
+// wait_stage where each of STEPS steps may be on its way, with A + B copies of this wavefront's each: A of x, at most PER.
+template <int STEPS, int PER, int B>
+__device__ __forceinline__ void wait_steps(int a) {
+  static_assert(PER <= 4, "cases");
+  if (PER >= 4 && a == 4) wait_stage<STEPS * (4 + B)>();
+  else if (PER >= 3 && a == 3) wait_stage<STEPS * (3 + B)>();
+  else if (PER >= 2 && a == 2) wait_stage<STEPS * (2 + B)>();
+  else if (a == 1) wait_stage<STEPS * (1 + B)>();
+  else wait_stage<STEPS * B>();
+}
 
 // The accumulators of a tile go through LDS as fp32 rows (padded by 16 bytes), so that each thread finishes 8 consecutive
 // columns with 16-byte loads and stores.
@@ -415,20 +430,20 @@ __global__ __launch_bounds__(WT * WN * 64) void grouped_tile_kernel(GroupedArgs 
   const int nk = (a.K + 63) / 64, tail = a.K - (nk - 1) * 64;
   const int64_t sb = BK ? 128 : 64 * ldb;
   const uint32_t lds0 = lds_addr(lds);
+  const int exist = min(BT, a.T - t0), n_a = decltype(oa)::copies(wave, exist);        // rows of the tile that are there
   auto fetch = [&](int k) {
     const uint32_t st = lds0 + k % NST * kStage;
     const bool whole = k < nk - 1 || tail == 64;
-    oa.copy(st, wave, (int64_t)k * 128, whole ? 128 : tail * 2);
+    oa.copy(st, wave, (int64_t)k * 128, whole ? 128 : tail * 2, n_a);
     if (whole) ob.copy(st + kA, wave, pb + k * sb);
     else ob.copy_tail(st + kA, wave, pb + k * sb, BK ? tail * 2 : tail);
   };
-  constexpr int kCopies = decltype(oa)::kMin + decltype(ob)::kMin;
   f32x4_t acc[FT][FN];
 #pragma unroll
   for (int i = 0; i < FT; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int blocks = __builtin_amdgcn_readfirstlane((min(BT, a.T - t0) + 15) / 16 - wt * FT);   // this wavefront's that exist
+  const int blocks = __builtin_amdgcn_readfirstlane((exist + 15) / 16 - wt * FT);   // this wavefront's that exist
   auto multiply = [&](const char* st, int upto) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -451,7 +466,7 @@ __global__ __launch_bounds__(WT * WN * 64) void grouped_tile_kernel(GroupedArgs 
   for (int k = 0; k < NST - 1; ++k)
     if (k < nk) fetch(k);
   for (int k = 0; k < nk; ++k) {
-    if (NST > 2 && k + NST - 1 <= nk) wait_stage<(NST - 2) * kCopies>();
+    if (NST > 2 && k + NST - 1 <= nk) wait_steps<NST - 2, decltype(oa)::kPer, decltype(ob)::kMin>(n_a);
     else wait_stage<0>();
     const char* st = lds + k % NST * kStage;
     if (k + NST - 1 < nk) fetch(k + NST - 1);
@@ -812,18 +827,19 @@ __global__ __launch_bounds__(CW * KW * 64) void grouped_few_kernel(GroupedArgs g
 
 // ------------------------------------------------------------------ 4-bit products of many rows
 //
-// The tile kernel with codes for weights: steps of 64 k, x's 128 bytes a row and the codes' 32 copied straight into
-// LDS, the codes decoded by the wavefront that multiplies them.  A row's two 16-byte halves are exchanged in every other
-// eight rows, so that the 16 rows of one read fall on all banks.  The scales of 1024 k lie in LDS as well (int4 as fp32
-// by group, MXFP4 as bytes by row); those of the next 1024 wait in registers while these are used.
+// The tile kernel with codes for weights: steps of 128 k in two halves, x's 128 bytes a row and half and the codes' 32
+// copied straight into LDS, the codes decoded by the wavefront that multiplies them.  A row's two 16-byte parts of a half
+// are exchanged in every other eight rows, so that the 16 rows of one read fall on all banks.  The scales of 1024 k lie
+// in LDS as well (int4 as fp32 by group, MXFP4 as bf16 by row); those of the next 1024 wait in registers while these are
+// used.
 template <DenseOp OP, int WTYPE, int WT, int WN, int FT, int FN, int NST>
 __global__ __launch_bounds__(WT * WN * 64) void quant_tile_kernel(GroupedArgs g) {
   constexpr int NW = WT * WN, BT = WT * FT * 16, BN = WN * FN * 16, kThreads = NW * 64;
   constexpr int NO = OP == DENSE_GLU ? BN / 2 : BN;
-  constexpr int kA = BT * 128, kB = BN * 32, kStage = kA + kB;
-  constexpr int kChunk = 16;                             // steps that share a stretch of scales
+  constexpr int kA = BT * 128, kB = BN * 32, kHalf = kA + kB, kStage = 2 * kHalf;
+  constexpr int kChunk = 8;                              // steps that share a stretch of scales
   constexpr int kGroups = kInt4<WTYPE> ? 8 : 32;         // scales of a row in it
-  constexpr int kRow = kInt4<WTYPE> ? 4 * BN : 36;       // bytes from group to group, from row to row
+  constexpr int kRow = kInt4<WTYPE> ? 4 * BN : 68;       // bytes from group to group, from row to row
   // scales a thread holds: one fp16 each, or four bytes
   constexpr int kHeld = BN * kGroups / (kInt4<WTYPE> ? 1 : 4) / kThreads;
   static_assert(kHeld * kThreads * (kInt4<WTYPE> ? 1 : 4) == BN * kGroups, "threads hold whole shares");
@@ -844,31 +860,34 @@ __global__ __launch_bounds__(WT * WN * 64) void quant_tile_kernel(GroupedArgs g)
   };
   RowOperand<BT, NW> oa;
   oa.init(wave, lane, [&](int r) { return static_cast<const char*>(a.a) + x_row(g, min(t0 + r, a.T - 1)) * a.lda * 2; });
-  constexpr int kCodes = BN / 32, kCodesPer = (kCodes + NW - 1) / NW, kCodesMin = kCodes / NW;   // 1024-byte copies a step
+  constexpr int kCodes = BN / 32, kCodesPer = (kCodes + NW - 1) / NW, kCodesMin = kCodes / NW;   // 1024-byte copies a half
   static_assert(kCodes % NW == 0 || kCodesPer == 1, "copies divide evenly, or go one each to the first");
   const char* codes[kCodesPer];
-  int half[kCodesPer];
+  int part[kCodesPer];
 #pragma unroll
   for (int i = 0; i < kCodesPer; ++i) {
     const int r = 32 * (wave + i * NW) + (lane >> 1);
-    half[i] = ((lane & 1) ^ ((r >> 3) & 1)) * 16;
-    codes[i] = static_cast<const char*>(a.b) + w_row(min(r, BN - 1)) * (K / 2) + half[i];
+    part[i] = ((lane & 1) ^ ((r >> 3) & 1)) * 16;
+    codes[i] = static_cast<const char*>(a.b) + w_row(min(r, BN - 1)) * (K / 2) + part[i];
   }
   Frags<BT, true, FT> fa;
   fa.init(wt * FT * 16, lane);
-  const int nk = (K + 63) / 64, tail = K - (nk - 1) * 64;
+  const int nk = (K + 127) / 128;
   const uint32_t lds0 = lds_addr(lds);
+  const int exist = min(BT, a.T - t0), n_a = decltype(oa)::copies(wave, exist);        // rows of the tile that are there
   auto fetch = [&](int k) {
-    const uint32_t st = lds0 + k % NST * kStage;
-    const int valid = k < nk - 1 ? 64 : tail;
-    oa.copy(st, wave, (int64_t)k * 128, valid * 2);
 #pragma unroll
-    for (int i = 0; i < kCodesPer; ++i)
-      if (kCodesMin == kCodesPer || wave < kCodes)
-        copy_to_lds(st + kA + (wave + i * NW) * 1024,
-                    half[i] < valid / 2 ? codes[i] + (int64_t)k * 32 : reinterpret_cast<const char*>(g_zeros));
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t st = lds0 + k % NST * kStage + h * kHalf;
+      const int at = 128 * k + 64 * h, valid = min(max(K - at, 0), 64);
+      oa.copy(st, wave, (int64_t)at * 2, valid * 2, n_a);
+#pragma unroll
+      for (int i = 0; i < kCodesPer; ++i)
+        if (kCodesMin == kCodesPer || wave < kCodes)
+          copy_to_lds(st + kA + (wave + i * NW) * 1024,
+                      part[i] < valid / 2 ? codes[i] + at / 2 : reinterpret_cast<const char*>(g_zeros));
+    }
   };
-  constexpr int kCopies = decltype(oa)::kMin + kCodesMin;
   // this thread's scales of chunk c: thread after thread along the rows
   uint32_t held[kHeld];
   const bool words = K % 128 == 0;                       // MXFP4 rows of whole words
@@ -898,8 +917,16 @@ __global__ __launch_bounds__(WT * WN * 64) void quant_tile_kernel(GroupedArgs g)
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
       const int idx = threadIdx.x + i * kThreads;
-      if constexpr (kInt4<WTYPE>) *reinterpret_cast<float*>(scales + idx % 8 * kRow + idx / 8 * 4) = half_value((uint16_t)held[i]);
-      else *reinterpret_cast<uint32_t*>(scales + idx / 8 * kRow + idx % 8 * 4) = held[i];
+      if constexpr (kInt4<WTYPE>) {
+        *reinterpret_cast<float*>(scales + idx % 8 * kRow + idx / 8 * 4) = half_value((uint16_t)held[i]);
+      } else {
+        uint32_t* at = reinterpret_cast<uint32_t*>(scales + idx / 8 * kRow + idx % 8 * 8);
+        uint32_t b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(e8m0(held[i] >> (8 * j) & 0xFF));
+        at[0] = b[0] >> 16 | (b[1] & 0xFFFF0000u);
+        at[1] = b[2] >> 16 | (b[3] & 0xFFFF0000u);
+      }
     }
   };
   f32x4_t acc[FT][FN];
@@ -907,50 +934,53 @@ __global__ __launch_bounds__(WT * WN * 64) void quant_tile_kernel(GroupedArgs g)
   for (int i = 0; i < FT; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int blocks = __builtin_amdgcn_readfirstlane((min(BT, a.T - t0) + 15) / 16 - wt * FT);
+  const int blocks = __builtin_amdgcn_readfirstlane((exist + 15) / 16 - wt * FT);
   auto multiply = [&](int k, int upto) {
     const char* st = lds + k % NST * kStage;
-    const char* cw = st + kA + (wn * FN * 16 + ln) * 32 + 4 * q;
-    bf16x8_t bf[FN][2];
+    // codes of 32 k, the s-th of the step, of fragment j
+    auto weights = [&](int j, int s) {
+      const int r = (wn * FN + j) * 16 + ln;
+      const uint32_t d = *reinterpret_cast<const uint32_t*>(st + (s >> 1) * kHalf + kA + r * 32 + (((s & 1) ^ (ln >> 3)) << 4) + 4 * q);
+      float scale = 0.f;
+      if constexpr (kMx<WTYPE>)
+        scale = bf16_to_f32(*reinterpret_cast<const uint16_t*>(scales + r * kRow + (k % kChunk * 4 + s) * 2));
+      return decode8<WTYPE>(d, scale);
+    };
+    bf16x8_t bf[FN][4];
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const uint32_t d = *reinterpret_cast<const uint32_t*>(cw + j * 512 + ((s ^ (ln >> 3)) << 4));
-        float scale = 0.f;
-        if constexpr (kMx<WTYPE>)
-          scale = e8m0(*reinterpret_cast<const uint8_t*>(scales + ((wn * FN + j) * 16 + ln) * kRow + k % kChunk * 2 + s));
-        bf[j][s] = decode8<WTYPE>(d, scale);
-      }
+      for (int s = 0; s < 4; ++s) bf[j][s] = weights(j, s);
     f32x4_t sc[kInt4<WTYPE> ? FN : 1];
     if constexpr (kInt4<WTYPE>) {
 #pragma unroll
       for (int j = 0; j < FN; ++j)
-        sc[j] = *reinterpret_cast<const f32x4_t*>(scales + k % kChunk / 2 * kRow + ((wn * FN + j) * 16 + 4 * q) * 4);
+        sc[j] = *reinterpret_cast<const f32x4_t*>(scales + k % kChunk * kRow + ((wn * FN + j) * 16 + 4 * q) * 4);
     }
 #pragma unroll
     for (int i = 0; i < FT; ++i) {
       if (i >= upto) continue;
-      bf16x8_t af[2];
+      bf16x8_t af[4];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) af[s] = fa.bf16(st, i, s);
+      for (int s = 0; s < 4; ++s) af[s] = fa.bf16(st + (s >> 1) * kHalf, i, s & 1);
       if constexpr (kInt4<WTYPE>) {
         f32x4_t start = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int s = 0; s < 2; ++s) start = __builtin_amdgcn_mfma_f32_16x16x32_bf16(minus8(), af[s], start, 0, 0, 0);
+        for (int s = 0; s < 4; ++s) start = __builtin_amdgcn_mfma_f32_16x16x32_bf16(minus8(), af[s], start, 0, 0, 0);
+        f32x4_t p[FN];
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          f32x4_t p = start;
+        for (int s = 0; s < 4; ++s)
 #pragma unroll
-          for (int s = 0; s < 2; ++s) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j][s], af[s], p, 0, 0, 0);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[e], sc[j][e], acc[i][j][e]);
-        }
-      } else {
+          for (int j = 0; j < FN; ++j) p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j][s], af[s], s ? p[j] : start, 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
-          for (int s = 0; s < 2; ++s)
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[j][e], sc[j][e], acc[i][j][e]);
+      } else {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j][s], af[s], acc[i][j], 0, 0, 0);
       }
     }
@@ -965,7 +995,7 @@ __global__ __launch_bounds__(WT * WN * 64) void quant_tile_kernel(GroupedArgs g)
       place();
     }
     // (scales being fetched only make this wait for more)
-    if (NST > 2 && k + NST - 1 <= nk) wait_stage<(NST - 2) * kCopies>();
+    if (NST > 2 && k + NST - 1 <= nk) wait_steps<2 * (NST - 2), decltype(oa)::kPer, kCodesMin>(n_a);
     else wait_stage<0>();
     if (k + NST - 1 < nk) fetch(k + NST - 1);
     if (k % kChunk == 0 && k + kChunk < nk) hold(k / kChunk + 1);
@@ -996,7 +1026,7 @@ void launch_rows(const GroupedArgs& a, hipStream_t s) {
 template <DenseOp OP, int WTYPE, int WT, int WN, int FT, int FN, int NST>
 void launch_quant(const GroupedArgs& a, hipStream_t s) {
   constexpr int BT = WT * FT * 16, BN = WN * FN * 16, NO = OP == DENSE_GLU ? BN / 2 : BN;
-  constexpr int kLds = std::max(NST * (BT * 128 + BN * 32) + BN * (kInt4<WTYPE> ? 32 : 36), BT * (BN + 4) * 4);
+  constexpr int kLds = std::max(NST * 2 * (BT * 128 + BN * 32) + BN * (kInt4<WTYPE> ? 32 : 68), BT * (BN + 4) * 4);
   static_assert(kLds <= 160 * 1024, "LDS of one workgroup");
   const int64_t tiles = row_tiles(a, BT) * ((a.d.N + NO - 1) / NO);
   quant_tile_kernel<OP, WTYPE, WT, WN, FT, FN, NST><<<dim3((unsigned)tiles), WT * WN * 64, kLds, s>>>(a);
@@ -1009,25 +1039,46 @@ void launch_few(const GroupedArgs& a, hipStream_t s) {
       <<<dim3((a.d.N + NO - 1) / NO, (unsigned)row_tiles(a, NR)), CW * KW * 64, 0, s>>>(a);
 }
 
+// us of the two sides of each choice, at rows x columns x k, with `E x rows` where they are grouped.
 template <DenseOp OP, int WTYPE>
 void launch_sized(const GroupedArgs& a, hipStream_t s) {
-  const int rows = a.offsets ? a.R / std::min(a.E, a.R) : a.R;    // of a matrix
-  if (rows <= 32 && row_tiles(a, 8) < 65536) {
-    auto blocks = [&](int nr, int cols) { return row_tiles(a, nr) * ((a.d.N + cols - 1) / cols); };
-    if constexpr (OP == DENSE_GLU) {
+  constexpr bool GLU = OP == DENSE_GLU, Q = WTYPE != PE_W_BF16;
+  const int rows = a.offsets ? a.R / std::min(a.E, a.R) : a.R;    // of a matrix, on average
+  auto blocks = [&](int nr, int cols) { return row_tiles(a, nr) * ((a.d.N + cols - 1) / cols); };
+  // Streaming reads the weights once for every 16 rows, and is over when its workgroups are: grouped, 128 x 2 to 4 rows of
+  // GLU 768 x 2048 in int4 35 and 62, tiles 55 and 57; of one matrix, 96 x 2048 x 6144 25 against 34, 48 x 6144 x 2048 14.0
+  // and 14.0, GLU of 32 x 6144 x 2048 14.8 and 14.8 (576 and 768 workgroups), of 128 x 768 x 2048 10.4 against 14.0.
+  if (a.offsets ? rows < 4 : blocks(16, GLU ? 16 : 32) <= 576) {
+    if constexpr (GLU) {
+      // 16 rows, or 8 and two parts of k; where those are many, two workgroups' work in one (4 rows for 30 experts, int4
+      // 768 x 2048: 15.0 against 15.6; bf16 41.7 against 38.6)
       if (rows > 8) launch_few<OP, WTYPE, 2, 1, 4, 1, 2>(a, s);
-      else if (WTYPE == PE_W_BF16 || blocks(8, 8) <= 1024) launch_few<OP, WTYPE, 2, 1, 4, 2, 2>(a, s);
+      else if (!Q || blocks(8, 8) <= 1024) launch_few<OP, WTYPE, 2, 1, 4, 2, 2>(a, s);
       else launch_few<OP, WTYPE, 2, 2, 2, 2, 2>(a, s);
     } else {
+      // short sums: wavefronts for columns rather than for parts of k (30 experts, int4 2048 x 768: 10.0 against 11.5)
       if (a.d.K <= 1024) launch_few<OP, WTYPE, 2, 2, 2, 1, 3>(a, s);
+      // the smallest workgroups while they are few (1 x 2048 x 6144: 4.4 against 5.4), 32 columns where those
+      // make 128 (16 x 6144 x 2048: 5.9 against 7.3), two parts of k otherwise (16 x 2048 x 6144: 7.4 against 11)
       else if (rows <= 8 && blocks(8, 8) <= 512) launch_few<OP, WTYPE, 1, 1, 4, 2, 2>(a, s);
       else if (blocks(16, 32) >= 128) launch_few<OP, WTYPE, 2, 1, 4, 1, 2>(a, s);
       else launch_few<OP, WTYPE, 2, 1, 4, 2, 2>(a, s);
     }
     return;
   }
-  if constexpr (WTYPE == PE_W_BF16) launch_rows<OP, true, 2, 4, 4, 2, 2>(a, s);
-  else launch_quant<OP, WTYPE, 2, 4, 4, 2, 3>(a, s);
+  if constexpr (Q) {
+    // 16 x 128 for few rows (128 experts of 8, GLU 768 x 2048: 57 against 66; of 24: 87 and 85; 256 x 2048 x 2048: 14
+    // against 18), 128 x 256 where those fill the units (4096 x 6144 x 6144: 381 against 478), 64 x 128 otherwise (2048 x
+    // 2048 x 6144: 67 against 100)
+    const int cols = GLU ? 64 : 128;
+    if (a.offsets ? rows <= 16 : blocks(64, cols) < 128) launch_quant<OP, WTYPE, 1, 4, 1, 2, 3>(a, s);
+    else if (rows >= 256 && blocks(128, 2 * cols) >= 256) launch_quant<OP, WTYPE, 2, 4, 4, 4, 2>(a, s);
+    else launch_quant<OP, WTYPE, 2, 4, 2, 2, 2>(a, s);
+  } else {
+    // 64 x 128 in four stages for few rows (8 experts of 64, GLU 768 x 2048: 19.7 against 26.3; 128 of 128: 284 against 227)
+    if (rows <= 96) launch_rows<OP, true, 2, 4, 2, 2, 4>(a, s);
+    else launch_rows<OP, true, 4, 2, 2, 4, 2>(a, s);
+  }
 }
 
 }  // namespace
@@ -1046,8 +1097,12 @@ void launch_grouped(DenseOp op, int wtype, const GroupedArgs& a, hipStream_t s) 
 }
 
 void launch_grouped_back(DenseOp op, const GroupedArgs& a, hipStream_t s) {
-  if (op == DENSE_DGLU) launch_rows<DENSE_DGLU, false, 2, 4, 4, 2, 2>(a, s);
-  else launch_rows<DENSE_LINEAR, false, 2, 4, 4, 2, 2>(a, s);
+  // as in launch_sized (8 experts of 64: dh 21.3 against 31.2, dx 15.5 against 21.3; 128 of 128: dh 178 against 153)
+  const bool small = a.R / std::min(a.E, a.R) <= 96;
+  if (op == DENSE_DGLU && small) launch_rows<DENSE_DGLU, false, 2, 4, 2, 2, 4>(a, s);
+  else if (op == DENSE_DGLU) launch_rows<DENSE_DGLU, false, 4, 2, 2, 4, 2>(a, s);
+  else if (small) launch_rows<DENSE_LINEAR, false, 2, 4, 2, 2, 4>(a, s);
+  else launch_rows<DENSE_LINEAR, false, 4, 2, 2, 4, 2>(a, s);
 }
 
 namespace {

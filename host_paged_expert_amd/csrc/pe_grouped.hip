@@ -1048,13 +1048,21 @@ void launch_sized(const GroupedArgs& a, hipStream_t s) {
   // Streaming reads the weights once for every 16 rows, and is over when its workgroups are: grouped, 128 x 2 to 4 rows of
   // GLU 768 x 2048 in int4 35 and 62, tiles 55 and 57; of one matrix, 96 x 2048 x 6144 25 against 34, 48 x 6144 x 2048 14.0
   // and 14.0, GLU of 32 x 6144 x 2048 14.8 and 14.8 (576 and 768 workgroups), of 128 x 768 x 2048 10.4 against 14.0.
-  if (a.offsets ? rows < 4 : blocks(16, GLU ? 16 : 32) <= 576) {
+  if (a.offsets ? rows < 4 && blocks(8, 8) < 1 << 24 : blocks(16, GLU ? 16 : 32) <= 576) {
     if constexpr (GLU) {
       // 16 rows, or 8 and two parts of k; where those are many, two workgroups' work in one (4 rows for 30 experts, int4
-      // 768 x 2048: 15.0 against 15.6; bf16 41.7 against 38.6)
-      if (rows > 8) launch_few<OP, WTYPE, 2, 1, 4, 1, 2>(a, s);
-      else if (!Q || blocks(8, 8) <= 1024) launch_few<OP, WTYPE, 2, 1, 4, 2, 2>(a, s);
-      else launch_few<OP, WTYPE, 2, 2, 2, 2, 2>(a, s);
+      // 768 x 2048: 15.0 against 15.6; bf16 41.7 against 38.6).  (bf16 comes here grouped alone, with fewer rows.)
+      if constexpr (Q) {
+        if (rows > 8) {
+          launch_few<OP, WTYPE, 2, 1, 4, 1, 2>(a, s);
+          return;
+        }
+        if (blocks(8, 8) > 1024) {
+          launch_few<OP, WTYPE, 2, 2, 2, 2, 2>(a, s);
+          return;
+        }
+      }
+      launch_few<OP, WTYPE, 2, 1, 4, 2, 2>(a, s);
     } else {
       // short sums: wavefronts for columns rather than for parts of k (30 experts, int4 2048 x 768: 10.0 against 11.5)
       if (a.d.K <= 1024) launch_few<OP, WTYPE, 2, 2, 2, 1, 3>(a, s);

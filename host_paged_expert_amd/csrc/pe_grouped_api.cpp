@@ -13,11 +13,15 @@
 
 namespace {
 
-// A launch has fewer than 2^24 workgroups of up to 256 threads; the products' smallest take 16 rows and 16 columns.
-int check_tiles(int64_t rows, int64_t matrices, int64_t cols) {
-  const int64_t tiles = (rows / 16 + matrices + 1) * ((cols + 15) / 16);
-  if (tiles >= (1 << 24)) return fail(PE_ERR_INVALID_ARG, "%lld rows of %lld columns are too many for one call", (long long)rows, (long long)cols);
+// A launch has fewer than 2^32 threads, so fewer than 2^23 workgroups of 512.  The products' smallest tiles are 16 x 64,
+// the weight gradients' 128 x 128 for each matrix.
+int check_tiles(int64_t tiles) {
+  if (tiles >= (1 << 23)) return fail(PE_ERR_INVALID_ARG, "the matrices are too large for one call");
   return PE_OK;
+}
+int64_t row_tiles(int64_t rows, int64_t matrices, int64_t cols) { return (rows / 16 + matrices + 1) * ((cols + 63) / 64); }
+int64_t weight_tiles(int64_t matrices, int64_t rows, int64_t cols) {
+  return matrices * (((rows + 127) / 128 * ((cols + 127) / 128) + 7) / 8 * 8);
 }
 
 int check_experts(int num_experts) {
@@ -84,7 +88,7 @@ int pe_linear_w4(int device, int wtype, const void* x, int64_t ldx, const void* 
   PE_TRY(check_mat(mb, true));
   PE_TRY(check_mat(mr, true));
   PE_TRY(check_mat(my, false));
-  PE_TRY(check_tiles(T, 1, N));
+  PE_TRY(check_tiles(row_tiles(T, 1, N)));
   PE_TRY(check_apart({{&my, {&mr}}}, {&mx, &mw.w, &mw.s, &mb, &mr}));
   DeviceScope dev(device);
   PE_HIP(dev.err);
@@ -110,7 +114,7 @@ int pe_glu_w4(int device, int wtype, int act, const void* x, int64_t ldx, const 
   PE_TRY(check_weights("w13", "s13", wtype, w13, s13, 1, 2 * (int64_t)I, H, false, &mw));
   PE_TRY(check_mat(mx, false));
   PE_TRY(check_mat(mh, false));
-  PE_TRY(check_tiles(T, 1, 2 * (int64_t)I));
+  PE_TRY(check_tiles(row_tiles(T, 1, I)));
   PE_TRY(check_apart({{&mh, {}}}, {&mx, &mw.w, &mw.s}));
   DeviceScope dev(device);
   PE_HIP(dev.err);
@@ -166,7 +170,7 @@ int pe_grouped_linear(int device, int wtype, const void* x, int64_t ldx, int x_r
   PE_TRY(check_mat(mo, false));
   PE_TRY(check_mat(mb, true));
   PE_TRY(check_mat(my, false));
-  PE_TRY(check_tiles(R, E, N));
+  PE_TRY(check_tiles(row_tiles(R, E, N)));
   PE_TRY(check_apart({{&my, {}}}, {&mx, &mrow, &mo, &mw.w, &mw.s, &mb}));
   DeviceScope dev(device);
   PE_HIP(dev.err);
@@ -199,7 +203,7 @@ int pe_grouped_glu(int device, int wtype, int act, const void* x, int64_t ldx, i
   PE_TRY(check_mat(mo, false));
   PE_TRY(check_mat(mh, false));
   PE_TRY(check_mat(mg, true));
-  PE_TRY(check_tiles(R, E, 2 * (int64_t)I));
+  PE_TRY(check_tiles(row_tiles(R, E, I)));
   PE_TRY(check_apart({{&mh, {}}, {&mg, {}}}, {&mx, &mrow, &mo, &mw.w, &mw.s}));
   DeviceScope dev(device);
   PE_HIP(dev.err);
@@ -302,10 +306,10 @@ int pe_grouped_ffn_backward(int device, int act, const void* dy, int64_t lddy, c
       PE_TRY(check_mat(mx, false));
     }
     if ((uintptr_t)rows % 4) return fail(PE_ERR_INVALID_ARG, "rows must be a multiple of 4 bytes");
-    PE_TRY(check_tiles(R, E, std::max<int64_t>(H, I)));
+    PE_TRY(check_tiles(row_tiles(R, E, std::max(H, I))));
   }
-  PE_TRY(check_tiles(E * I2, 1, H));
-  PE_TRY(check_tiles((int64_t)E * H, 1, I));
+  PE_TRY(check_tiles(weight_tiles(E, I2, H)));
+  PE_TRY(check_tiles(weight_tiles(E, H, I)));
   PE_TRY(check_apart({{&mdgu, {}}, {&mh, {}}, {&mdx, {}}, {&mdw13, {}}, {&mdw2, {}}},
                      {&mdy, &mx, &mgu, &mrow, &mo, &mw13, &mw2}));
   DeviceScope dev(device);

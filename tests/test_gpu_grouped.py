@@ -11,6 +11,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+import gradient_bounds
 import host_paged_expert_amd as pe
 from oracle import dense, formats, grouped
 from test_gpu_dense import BF, DEV, FN, GUARD, _backward_bounds, _bf, _np, _padded, _strided, _within
@@ -442,6 +443,217 @@ def test_no_rows():
                             dw13=d13, dw2=d2)
     torch.cuda.synchronize()
     assert not d13.any() and not d2.any()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gradients_against_differences(act):
+    """Every coordinate of the gradients against the difference of the 64-bit forward at two points beside it."""
+    T, H, I, E = 5, 16, 8, 3
+    counts = [5, 0, 5]
+    points = [gradient_bounds.point(T, H, I, act, e, lambda a: torch.from_numpy(a).to(torch.bfloat16).double().numpy())
+              for e in range(E)]
+    x, dy = (_bf(np.concatenate([points[e][i] for e in (0, 2)]))[0] for i in (0, 3))
+    w13, w2 = (_bf(np.stack([p[i] for p in points]))[0] for i in (1, 2))
+    e = lambda *s: torch.empty(s, dtype=torch.bfloat16, device=DEV)           # noqa: E731
+    R, o = sum(counts), _i32(np.concatenate([[0], np.cumsum(counts)]))
+    h, gu, dgu, h2, dx, d13, d2 = e(R, I), e(R, 2 * I), e(R, 2 * I), e(R, I), e(R, H), e(E, 2 * I, H), e(E, H, I)
+    pe.grouped_glu(x, w13, h, o, act=act, gu=gu)
+    pe.grouped_ffn_backward(dy, x, gu, w13, w2, o, dgu, h=h2, dx=dx, dw13=d13, dw2=d2, act=act)
+    torch.cuda.synchronize()
+    for n, k in enumerate((0, 2)):
+        diffs, bounds = gradient_bounds.differences(*points[k], act), gradient_bounds.bounds(*points[k], act)
+        for got, ref, tol in zip((dx[5 * n:5 * n + 5], d13[k], d2[k]), diffs, bounds):
+            _within(_np(got), ref, tol, "expert %d" % k)
+    assert not d13[1].any() and not d2[1].any()
+
+
+# ------------------------------------------------------------------ on both sides of every choice of kernel
+
+def _some(rng, n, count):
+    return np.unique(np.concatenate([[0, n - 1, n // 2], rng.integers(0, n, count)]))
+
+
+WAYS_LINEAR = [(1, 2048, 1152), (8, 4096, 1152), (8, 4104, 1152), (16, 6144, 1152), (16, 2048, 1152), (17, 700, 1024),
+               (144, 2048, 1152), (150, 2048, 1152), (200, 2048, 2176), (500, 2048, 256), (1000, 2048, 256),
+               (2048, 4096, 256), (2300, 4100, 384), (255, 33000, 128)]
+WAYS_GLU = [(4, 768, 1152), (9, 768, 1152), (16, 776, 1152), (8, 8192, 256), (8, 8208, 256), (144, 1024, 1152),
+            (200, 1024, 2176), (500, 1024, 256), (1000, 1024, 256), (2048, 2048, 256), (2300, 2056, 384)]
+
+
+@pytest.mark.parametrize("T,N,K", WAYS_LINEAR)
+@pytest.mark.parametrize("wtype", ["int4", "mxfp4"])
+def test_linear_w4_where_its_ways_change(T, N, K, wtype):
+    rng = np.random.default_rng(T + N + K)
+    x, xv = _bf(rng.standard_normal((T, K)))
+    w, s, wv, size = _weights(rng, wtype, (N, K))
+    res, rv = _bf(rng.standard_normal((T, N)))
+    out, ok = _padded(T, N)
+    pe.linear_w4(x, w, s, out, residual=res)
+    torch.cuda.synchronize()
+    r, c = _some(rng, T, 60), _some(rng, N, 60)
+    _check_linear(_np(out)[np.ix_(r, c)], xv[r], wv[c], size[c], _terms(wtype, K), residual=rv[np.ix_(r, c)])
+    ok()
+
+
+@pytest.mark.parametrize("T,I,H", WAYS_GLU)
+@pytest.mark.parametrize("wtype", ["int4", "mxfp4"])
+def test_glu_w4_where_its_ways_change(T, I, H, wtype):
+    rng = np.random.default_rng(T + I + H)
+    x, xv = _bf(rng.standard_normal((T, H)))
+    w, s, wv, size = _weights(rng, wtype, (2 * I, H))
+    out, ok = _padded(T, I)
+    pe.glu_w4(x, w, s, out)
+    torch.cuda.synchronize()
+    r, c = _some(rng, T, 60), _some(rng, I, 60)
+    both = np.concatenate([c, I + c])
+    _check_glu(_np(out)[np.ix_(r, c)], None, xv[r], wv[both], size[both], _terms(wtype, H), "silu")
+    ok()
+
+
+# (experts, rows, columns, k): on average under 4 rows, up to 16, up to 96, more, 256 and more
+WAYS_GROUPED = [(3, 5, 64, 1152), (32, 97, 96, 1152), (40, 100, 2048, 1152), (30, 80, 8208, 256), (5, 12, 100, 256),
+                (4, 15, 200, 256), (4, 16, 200, 256), (4, 67, 200, 256), (4, 68, 200, 1152), (3, 290, 300, 256),
+                (3, 294, 300, 1152), (200, 2000, 136, 128), (2, 1100, 6704, 256), (130, 300, 72, 128), (1024, 900, 40, 128)]
+
+
+def _uneven(rng, E, R):
+    """Offsets of E experts that share R rows unevenly, some with none."""
+    cuts = np.sort(np.floor(R * rng.random(E - 1) ** 1.5).astype(np.int32))
+    return np.concatenate([[0], cuts, [R]]).astype(np.int32)
+
+
+@pytest.mark.parametrize("E,R,N,K", WAYS_GROUPED)
+@pytest.mark.parametrize("wtype", ["bf16", "int4", "mxfp4"])
+@pytest.mark.parametrize("glu", [False, True])
+def test_grouped_products_where_their_ways_change(E, R, N, K, wtype, glu):
+    rng = np.random.default_rng(E + R + N + K)
+    N = N // 2 // 8 * 8 if glu else N
+    F, X = (2 if glu else 1), 50
+    offsets = _uneven(rng, E, R)
+    rows = rng.integers(0, X, R).astype(np.int32)
+    x, xv = _bf(rng.standard_normal((X, K)))
+    w, s, wv, size = _weights(rng, wtype, (E, F * N, K))
+    out, ok = _padded(R, N)
+    if glu:
+        pe.grouped_glu(x, w, out, _i32(offsets), rows=_i32(rows), w_scales=s)
+    else:
+        pe.grouped_linear(x, w, out, _i32(offsets), rows=_i32(rows), w_scales=s)
+    torch.cuda.synchronize()
+    got = _np(out)
+    c = _some(rng, N, 50)
+    both = np.concatenate([c, N + c]) if glu else c
+    for e in np.unique(np.searchsorted(offsets, _some(rng, R, 12), side="right") - 1):
+        p = np.arange(offsets[e], offsets[e + 1])
+        p = p[_some(rng, len(p), 40)]
+        if glu:
+            _check_glu(got[np.ix_(p, c)], None, xv[rows[p]], wv[e][both], size[e][both], _terms(wtype, K), "silu")
+        else:
+            _check_linear(got[np.ix_(p, c)], xv[rows[p]], wv[e][c], size[e][c], _terms(wtype, K))
+    ok()
+
+
+@pytest.mark.parametrize("E,R,H,I", [(4, 387, 256, 136), (4, 388, 264, 128), (3, 700, 136, 264)])
+def test_grouped_ffn_backward_where_its_ways_change(E, R, H, I):
+    rng = np.random.default_rng(R)
+    offsets = _uneven(rng, E, R)
+    rows = rng.integers(0, 60, R).astype(np.int32)
+    x, xv = _bf(rng.standard_normal((60, H)))
+    w13, w13v = _bf(rng.standard_normal((E, 2 * I, H)) * 0.1)
+    w2, w2v = _bf(rng.standard_normal((E, H, I)) * 0.1)
+    dy, dyv = _bf(rng.standard_normal((R, H)))
+    gu, guv = _bf(rng.standard_normal((R, 2 * I)))
+    e = lambda *s: torch.full(s, GUARD, dtype=torch.bfloat16, device=DEV)     # noqa: E731
+    dgu, h, dx, d13, d2 = e(R, 2 * I), e(R, I), e(R, H), e(E, 2 * I, H), e(E, H, I)
+    pe.grouped_ffn_backward(dy, x, gu, w13, w2, _i32(offsets), dgu, rows=_i32(rows), h=h, dx=dx, dw13=d13, dw2=d2)
+    torch.cuda.synchronize()
+    for k, p in _parts(offsets):
+        refs, tols = _backward_bounds(xv[rows[p]], w13v[k], w2v[k], dyv[p], guv[p], "silu")
+        for name, got, ref, tol in zip(("dx", "dw13", "dw2"), (dx[p], d13[k], d2[k]), refs, tols):
+            _within(_np(got), ref, tol, "%s of expert %d" % (name, k))
+
+
+@pytest.mark.parametrize("T,k,E", [(128, 8, 70), (129, 8, 70), (16384, 8, 128), (16400, 8, 1024), (70000, 2, 3)])
+def test_group_rows_of_many_entries(T, k, E):
+    rng = np.random.default_rng(T + k)
+    ids = np.minimum(rng.integers(-1, E, (T, k)), rng.integers(0, E + 1, (T, k))).astype(np.int32)
+    flat = ids.ravel()
+    good = (flat >= 0) & (flat < E)
+    order = np.argsort(np.where(good, flat, E), kind="stable")[:good.sum()]
+    places = np.full(T * k, -1, np.int32)
+    places[order] = np.arange(len(order))
+    offsets, rows, at = (torch.full(s, 77, dtype=torch.int32, device=DEV) for s in ((E + 1,), (T * k,), (T, k)))
+    pe.group_rows(_i32(ids), offsets, rows, at)
+    torch.cuda.synchronize()
+    assert np.array_equal(offsets.cpu().numpy(), np.concatenate([[0], np.cumsum(np.bincount(flat[good], minlength=E))]))
+    assert np.array_equal(at.cpu().numpy().ravel(), places)
+    rows = rows.cpu().numpy()
+    assert np.array_equal(rows[:len(order)], order // k) and (rows[len(order):] == 77).all()
+
+
+# ------------------------------------------------------------------ matrices past 2^31 elements
+
+def test_weights_and_rows_past_32_bits():
+    """The last of many experts, rows of x and of y behind 2^31 elements, in the streaming kernels and in tiles."""
+    rng = np.random.default_rng(1)
+    E, N, K = 530, 1024, 4096                                    # 2.2e9 weights
+    w = torch.zeros((E, N, K), dtype=torch.bfloat16, device=DEV)
+    last, lv = _bf(rng.standard_normal((N, K)) * 0.1)
+    w[E - 1] = last
+    for R in (3, 2400):                                          # under 4 rows an expert, and more
+        x, xv = _bf(rng.standard_normal((8, K)))
+        o = np.zeros(E + 1, np.int32)
+        o[E] = R
+        o[E - 1] = R - 2
+        o[1:E - 1] = R - 2
+        rows = rng.integers(0, 8, R).astype(np.int32)
+        y = torch.full((R, N), GUARD, dtype=torch.bfloat16, device=DEV)
+        pe.grouped_linear(x, w, y, _i32(o), rows=_i32(rows))
+        torch.cuda.synchronize()
+        _check_linear(_np(y[R - 2:]), xv[rows[R - 2:]], lv, np.abs(lv), K)
+        assert not y[:R - 2].any()
+    del w
+    big = torch.zeros((600, 4000000), dtype=torch.bfloat16, device=DEV)       # rows 4e6 elements apart
+    x, y = big[:, :256], big[:, 1000000:1000064]
+    xs, xv = _bf(rng.standard_normal((600, 256)))
+    x.copy_(xs)
+    ws, wv = _bf(rng.standard_normal((2, 64, 256)))
+    pe.grouped_linear(x, ws, y, _i32([0, 599, 600]))
+    torch.cuda.synchronize()
+    _check_linear(_np(y[590:599]), xv[590:599], wv[0], np.abs(wv[0]), 256)
+    _check_linear(_np(y[599:]), xv[599:], wv[1], np.abs(wv[1]), 256)
+    q, s, qv, size = _weights(rng, "int4", (64, 256))
+    pe.linear_w4(x, q, s, y)
+    torch.cuda.synchronize()
+    _check_linear(_np(y[590:]), xv[590:], qv, size, _terms("int4", 256))
+    out = big[:, 2000000:2000256]
+    pe.combine(x, _i32(np.arange(600)[::-1].reshape(600, 1)), out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, x.flip(0))
+
+
+def test_weight_gradients_past_32_bits():
+    E, H, I = 270, 4096, 1024                                    # dw13: 2.3e9 elements
+    rng = np.random.default_rng(2)
+    dy, dyv = _bf(rng.standard_normal((5, H)))
+    x, xv = _bf(rng.standard_normal((5, H)))
+    gu, guv = _bf(rng.standard_normal((5, 2 * I)))
+    w2 = torch.zeros((E, H, I), dtype=torch.bfloat16, device=DEV)
+    last, lv = _bf(rng.standard_normal((H, I)) * 0.1)
+    w2[E - 1] = last
+    o = np.zeros(E + 1, np.int32)
+    o[E] = 5
+    d13 = torch.full((E, 2 * I, H), GUARD, dtype=torch.bfloat16, device=DEV)
+    d2 = torch.full((E, H, I), GUARD, dtype=torch.bfloat16, device=DEV)
+    dgu, h = torch.empty((5, 2 * I), dtype=torch.bfloat16, device=DEV), torch.empty((5, I), dtype=torch.bfloat16, device=DEV)
+    pe.grouped_ffn_backward(dy, x, gu, None, w2, _i32(o), dgu, h=h, dw13=d13, dw2=d2)
+    torch.cuda.synchronize()
+    dguv, hv = _np(dgu), _np(h)                                  # the products' own inputs
+    for got, left, right in ((d13[E - 1], dguv, xv), (d2[E - 1], dyv, hv)):
+        r, n = _some(rng, left.shape[1], 40), _some(rng, right.shape[1], 40)
+        ref = left[:, r].T @ right[:, n]
+        err = 13 * U * (np.abs(left[:, r]).T @ np.abs(right[:, n]))
+        _within(_np(got)[np.ix_(r, n)], ref, err + BF * (np.abs(ref) + err) + 1e-30)
+    assert not d13[:E - 1].any() and not d2[:E - 1].any()
 
 
 # ------------------------------------------------------------------ together

@@ -19,8 +19,9 @@ namespace pe {
 // A stable counting sort of the routed ids without scratch memory: every workgroup counts all ids by expert, those before
 // its own 64 NW PER apart, and so knows where its entries go without the others.  Among its own, a wavefront's come in
 // the order of its lanes (those of one expert find each other by a ballot for each bit of the id), wavefronts' in
-// theirs.  8192 x 8 ids, 128 experts: 8 us, a tenth of it for the bytes.  (A workgroup for each expert that numbers its
-// entries took 24: entries of one expert lie far apart, and each was a store of its own to lines that others write.)
+// theirs.  8192 x 8 ids, 128 experts: 11 us, where the bytes would take less than one: it is bound by the latency of its
+// passes, the counts' LDS atomics among them.  (A workgroup for each expert that numbers its entries took 24: entries of
+// one expert lie far apart, and each was a store of its own to lines that others write.)
 template <int NW, int PER>
 __global__ __launch_bounds__(NW * 64) void group_rows_kernel(GroupRowsArgs a) {
   constexpr int kThreads = NW * 64, kOwn = kThreads * PER, kBatch = 8;
@@ -130,7 +131,8 @@ void launch_group_rows(const GroupRowsArgs& a, hipStream_t s) {
 //
 // out[t] = sum_j w[t, j] y[places[t, j]] + residual[t], in fp32 and in the order of
 // j: LPR lanes share a token's stretch of 8 LPR columns, each with 8 of them and
-// four rows of y in flight.  Bound by its bytes, each once.
+// four rows of y in flight.  Bound by its bytes, each once: 8192 x 8 rows of 2048,
+// 336 MB, 68 us (4.9 TB/s, a large copy's rate).
 template <int LPR>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
   const int64_t t = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
@@ -175,7 +177,8 @@ void launch_combine(const CombineArgs& a, hipStream_t s) {
 
 // dy[places[t, j]] = w[t, j] dout[t] and dw[t, j] = sum_h dout[t, h] y[places[t, j], h]:
 // a wavefront per entry, which shares no sum with another.  Bound by its bytes;
-// dout comes from the caches but for a token's first entry.
+// dout comes from the caches but for a token's first entry (1023 x 4 rows of 2880:
+// 53 MB in 10.3 us, 5.1 TB/s).
 template <bool DY, bool DW>
 __global__ __launch_bounds__(256) void combine_back_kernel(CombineBackArgs a) {
   const int lane = threadIdx.x & 63;
@@ -263,7 +266,9 @@ __device__ __forceinline__ bool find_expert_tile(const GroupedArgs& a, int b, in
 #pragma unroll
   for (int i = 0; i < PER; ++i) mine += (max(o[i + 1] - o[i], 0) + BT - 1) / BT;
   const int upto = prefix_sum(mine);
-  const int total = __builtin_amdgcn_readlane(upto, 63) * nn;
+  const int row_tiles = __builtin_amdgcn_readlane(upto, 63);
+  if (row_tiles > a.R / BT + min(a.E, a.R)) return false;        // offsets that do not ascend
+  const int total = row_tiles * nn;
   if (b >= total) return false;
   int q = b;
   if constexpr (XCD) {
@@ -342,11 +347,16 @@ struct RowOperand {
   }
   // Copy the 128 bytes at byte `from` of each row, of which the first `valid` exist, in this many copies.
   __device__ __forceinline__ void copy(uint32_t lds, int wave, int64_t from, int valid, int n) const {
+    if (valid == 128) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (i < n)
-        copy_to_lds(lds + (wave + i * NW) * 1024,
-                    valid == 128 || kc[i] < valid ? at[i] + from : reinterpret_cast<const char*>(g_zeros));
+      for (int i = 0; i < kPer; ++i)
+        if (i < n) copy_to_lds(lds + (wave + i * NW) * 1024, at[i] + from);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i < n)
+          copy_to_lds(lds + (wave + i * NW) * 1024, kc[i] < valid ? at[i] + from : reinterpret_cast<const char*>(g_zeros));
+    }
   }
 };
 
@@ -397,8 +407,12 @@ __device__ __forceinline__ DenseArgs expert_args(const GroupedArgs& g, int e, in
 // ------------------------------------------------------------------ bf16 products of an expert's rows
 //
 // The tile of pe_dense.hip over an expert's rows: rows of x are fetched through the row list by the copies into LDS
-// themselves, weights K-major (forward) or k-slow (gradients).  An expert's last tile is partly empty; its wavefronts
-// skip the MFMAs of blocks of 16 rows that do not exist.
+// themselves, weights K-major (forward) or k-slow (gradients).  An expert's last tile is partly empty: rows that do not
+// exist are not copied, by eights, nor multiplied, by sixteens.  128 experts of 128 rows, uneven as a router leaves them, are
+// bound by the weights' bytes and by the operands' way from L2 into LDS, which is twice as many: GLU 768 x 2048, 805 MB
+// of weights, 222 us (4.0 TB/s with all it reads and writes); dh of the gradients 155, dx 230.  512 rows of 32 experts,
+// 2880 x 2880: 686 us, 0.79 PFLOP/s.  (A 256 x 192 tile of two groups of wavefronts in turn, the dense products' best,
+// is no faster here: 268 and 699 us.)
 template <DenseOp OP, bool BK, int WT, int WN, int FT, int FN, int NST>
 __global__ __launch_bounds__(WT * WN * 64) void grouped_tile_kernel(GroupedArgs g) {
   constexpr int NW = WT * WN, BT = WT * FT * 16, BN = WN * FN * 16;
@@ -480,7 +494,10 @@ __global__ __launch_bounds__(WT * WN * 64) void grouped_tile_kernel(GroupedArgs 
 //
 // out[e][m, n] = sum over expert e's rows r of left[r, m] right[r, n]: both operands are k-slow, k being the expert's
 // rows, and an expert without rows gets zeros.  Rows of x come through the row list: its part for the next 32 steps lies
-// in LDS, where the copies of a step find their rows' addresses.
+// in LDS, where the copies of a step find their rows' addresses.  With some hundred rows to an expert its gradient is
+// hardly more than its bytes written: 128 experts of 128 rows, 1536 x 2048, 805 MB in 305 us.  Epilogues alone take 133
+// (6 TB/s), the sums 173, and what is left is the one waiting for the other's memory.  (Workgroups that went through all
+// tiles of some columns with copies running ahead, with or without wavefronts of their own for the stores: 420 to 540.)
 template <bool GATHER, int WT, int WN, int FT, int FN, int NST>
 __global__ __launch_bounds__(WT * WN * 64) void grouped_weights_kernel(GroupedArgs g) {
   constexpr int NW = WT * WN, BT = WT * FT * 16, BN = WN * FN * 16, kList = 32;
@@ -661,6 +678,8 @@ __device__ __forceinline__ float half_value(uint16_t h) { return (float)__builti
 // their sums, which meet in LDS in a fixed order.  A step is 128 bytes of k in bf16 and 64 bytes, 128 k, in 4 bits.  P
 // parts of k share the MFMA's 16 x 16 block as in the dense kernel of few rows.  x is the first operand, so that a lane's
 // accumulators belong to one weight row and its scale.
+// One row of int4 2048 x 6144, 6.4 MB: 5.1 us, of which a launch that does nothing is some 2.5.  Four rows to 30 of 128
+// experts, int4 GLU 768 x 2048, 45 MB: 15 us (3 TB/s), bf16 177 MB: 37 us (4.8 TB/s).
 template <DenseOp OP, int WTYPE, int F, int CW, int KW, int P, int U>
 __global__ __launch_bounds__(CW * KW * 64) void grouped_few_kernel(GroupedArgs g) {
   static_assert(OP != DENSE_GLU || F == 2, "a gate and an up fragment");
@@ -830,8 +849,9 @@ __global__ __launch_bounds__(CW * KW * 64) void grouped_few_kernel(GroupedArgs g
 // The tile kernel with codes for weights: steps of 128 k in two halves, x's 128 bytes a row and half and the codes' 32
 // copied straight into LDS, the codes decoded by the wavefront that multiplies them.  A row's two 16-byte parts of a half
 // are exchanged in every other eight rows, so that the 16 rows of one read fall on all banks.  The scales of 1024 k lie
-// in LDS as well (int4 as fp32 by group, MXFP4 as bf16 by row); those of the next 1024 wait in registers while these are
-// used.
+// in LDS as well (as fp32, int4's by group, MXFP4's by row); those of the next 1024 wait in registers while these are
+// used.  2048 x 2048 x 6144: int4 81 us (0.63 PFLOP/s), MXFP4 61 (0.84); 4096 x 6144 x 6144 363 and 299 (0.85, 1.03): the
+// MFMAs that make -8 sum x are a quarter to a half of the others, and decoding costs as many cycles as they do.
 template <DenseOp OP, int WTYPE, int WT, int WN, int FT, int FN, int NST>
 __global__ __launch_bounds__(WT * WN * 64) void quant_tile_kernel(GroupedArgs g) {
   constexpr int NW = WT * WN, BT = WT * FT * 16, BN = WN * FN * 16, kThreads = NW * 64;
@@ -839,7 +859,7 @@ __global__ __launch_bounds__(WT * WN * 64) void quant_tile_kernel(GroupedArgs g)
   constexpr int kA = BT * 128, kB = BN * 32, kHalf = kA + kB, kStage = 2 * kHalf;
   constexpr int kChunk = 8;                              // steps that share a stretch of scales
   constexpr int kGroups = kInt4<WTYPE> ? 8 : 32;         // scales of a row in it
-  constexpr int kRow = kInt4<WTYPE> ? 4 * BN : 68;       // bytes from group to group, from row to row
+  constexpr int kRow = kInt4<WTYPE> ? 4 * BN : 144;      // bytes from group to group, from row to row
   // scales a thread holds: one fp16 each, or four bytes
   constexpr int kHeld = BN * kGroups / (kInt4<WTYPE> ? 1 : 4) / kThreads;
   static_assert(kHeld * kThreads * (kInt4<WTYPE> ? 1 : 4) == BN * kGroups, "threads hold whole shares");
@@ -876,16 +896,27 @@ __global__ __launch_bounds__(WT * WN * 64) void quant_tile_kernel(GroupedArgs g)
   const uint32_t lds0 = lds_addr(lds);
   const int exist = min(BT, a.T - t0), n_a = decltype(oa)::copies(wave, exist);        // rows of the tile that are there
   auto fetch = [&](int k) {
+    const uint32_t st = lds0 + k % NST * kStage;
+    const bool mine = kCodesMin == kCodesPer || wave < kCodes;
+    if (128 * k + 128 <= K) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t st = lds0 + k % NST * kStage + h * kHalf;
-      const int at = 128 * k + 64 * h, valid = min(max(K - at, 0), 64);
-      oa.copy(st, wave, (int64_t)at * 2, valid * 2, n_a);
+      for (int h = 0; h < 2; ++h) {
+        oa.copy(st + h * kHalf, wave, 256 * (int64_t)k + 128 * h, 128, n_a);
 #pragma unroll
-      for (int i = 0; i < kCodesPer; ++i)
-        if (kCodesMin == kCodesPer || wave < kCodes)
-          copy_to_lds(st + kA + (wave + i * NW) * 1024,
-                      part[i] < valid / 2 ? codes[i] + at / 2 : reinterpret_cast<const char*>(g_zeros));
+        for (int i = 0; i < kCodesPer; ++i)
+          if (mine) copy_to_lds(st + h * kHalf + kA + (wave + i * NW) * 1024, codes[i] + 64 * k + 32 * h);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = 128 * k + 64 * h, valid = min(max(K - at, 0), 64);
+        oa.copy(st + h * kHalf, wave, (int64_t)at * 2, valid * 2, n_a);
+#pragma unroll
+        for (int i = 0; i < kCodesPer; ++i)
+          if (mine)
+            copy_to_lds(st + h * kHalf + kA + (wave + i * NW) * 1024,
+                        part[i] < valid / 2 ? codes[i] + at / 2 : reinterpret_cast<const char*>(g_zeros));
+      }
     }
   };
   // this thread's scales of chunk c: thread after thread along the rows
@@ -920,12 +951,10 @@ __global__ __launch_bounds__(WT * WN * 64) void quant_tile_kernel(GroupedArgs g)
       if constexpr (kInt4<WTYPE>) {
         *reinterpret_cast<float*>(scales + idx % 8 * kRow + idx / 8 * 4) = half_value((uint16_t)held[i]);
       } else {
-        uint32_t* at = reinterpret_cast<uint32_t*>(scales + idx / 8 * kRow + idx % 8 * 8);
-        uint32_t b[4];
+        f32x4_t v;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(e8m0(held[i] >> (8 * j) & 0xFF));
-        at[0] = b[0] >> 16 | (b[1] & 0xFFFF0000u);
-        at[1] = b[2] >> 16 | (b[3] & 0xFFFF0000u);
+        for (int j = 0; j < 4; ++j) v[j] = e8m0(held[i] >> (8 * j) & 0xFF);
+        *reinterpret_cast<f32x4_t*>(scales + idx / 8 * kRow + idx % 8 * 16) = v;
       }
     }
   };
@@ -935,22 +964,20 @@ __global__ __launch_bounds__(WT * WN * 64) void quant_tile_kernel(GroupedArgs g)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const int blocks = __builtin_amdgcn_readfirstlane((exist + 15) / 16 - wt * FT);
+  // this lane's codes of the first 32 k of a half, and its scales, of fragment 0
+  const int code_at = kA + (wn * FN * 16 + ln) * 32 + ((ln >> 3) << 4) + 4 * q, scale_at = (wn * FN * 16 + ln) * kRow;
   auto multiply = [&](int k, int upto) {
     const char* st = lds + k % NST * kStage;
-    // codes of 32 k, the s-th of the step, of fragment j
-    auto weights = [&](int j, int s) {
-      const int r = (wn * FN + j) * 16 + ln;
-      const uint32_t d = *reinterpret_cast<const uint32_t*>(st + (s >> 1) * kHalf + kA + r * 32 + (((s & 1) ^ (ln >> 3)) << 4) + 4 * q);
-      float scale = 0.f;
-      if constexpr (kMx<WTYPE>)
-        scale = bf16_to_f32(*reinterpret_cast<const uint16_t*>(scales + r * kRow + (k % kChunk * 4 + s) * 2));
-      return decode8<WTYPE>(d, scale);
-    };
+    const char* const codes_at[2] = {st + code_at, st + (code_at ^ 16)};
     bf16x8_t bf[FN][4];
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
+    for (int j = 0; j < FN; ++j) {
+      f32x4_t scale = f32x4_t{0.f, 0.f, 0.f, 0.f};       // of the row's four blocks
+      if constexpr (kMx<WTYPE>) scale = *reinterpret_cast<const f32x4_t*>(scales + scale_at + j * 16 * kRow + k % kChunk * 16);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) bf[j][s] = weights(j, s);
+      for (int s = 0; s < 4; ++s)
+        bf[j][s] = decode8<WTYPE>(*reinterpret_cast<const uint32_t*>(codes_at[s & 1] + (s >> 1) * kHalf + j * 512), scale[s]);
+    }
     f32x4_t sc[kInt4<WTYPE> ? FN : 1];
     if constexpr (kInt4<WTYPE>) {
 #pragma unroll
@@ -1026,7 +1053,7 @@ void launch_rows(const GroupedArgs& a, hipStream_t s) {
 template <DenseOp OP, int WTYPE, int WT, int WN, int FT, int FN, int NST>
 void launch_quant(const GroupedArgs& a, hipStream_t s) {
   constexpr int BT = WT * FT * 16, BN = WN * FN * 16, NO = OP == DENSE_GLU ? BN / 2 : BN;
-  constexpr int kLds = std::max(NST * 2 * (BT * 128 + BN * 32) + BN * (kInt4<WTYPE> ? 32 : 68), BT * (BN + 4) * 4);
+  constexpr int kLds = std::max(NST * 2 * (BT * 128 + BN * 32) + BN * (kInt4<WTYPE> ? 32 : 144), BT * (BN + 4) * 4);
   static_assert(kLds <= 160 * 1024, "LDS of one workgroup");
   const int64_t tiles = row_tiles(a, BT) * ((a.d.N + NO - 1) / NO);
   quant_tile_kernel<OP, WTYPE, WT, WN, FT, FN, NST><<<dim3((unsigned)tiles), WT * WN * 64, kLds, s>>>(a);
@@ -1075,13 +1102,19 @@ void launch_sized(const GroupedArgs& a, hipStream_t s) {
     return;
   }
   if constexpr (Q) {
-    // 16 x 128 for few rows (128 experts of 8, GLU 768 x 2048: 57 against 66; of 24: 87 and 85; 256 x 2048 x 2048: 14
-    // against 18), 128 x 256 where those fill the units (4096 x 6144 x 6144: 381 against 478), 64 x 128 otherwise (2048 x
-    // 2048 x 6144: 67 against 100)
+    // The largest tile that still fills the units where a matrix has the rows for it: 128 x 256 (4096 x 6144 x 6144, int4:
+    // 363 against 441 in 128 x 128 and 462 in 64 x 128), 128 x 128 (2048 x 2048 x 6144: 81 against 90 in 32 x 128
+    // and 88 in 64 x 128).
+    // Below, 16 x 128 where one matrix makes few workgroups (256 x 2048 x 2048: 13.5 against 15.3 in 32 x 128; 1000 x 2880
+    // x 2816: 48 against 34), and 32 x 128, of which more fit in a unit, against 64 x 128: int4, 32 experts of 128
+    // rows, 2880 x 2816, 127 against 144, 128 of 8, GLU 768 x 2048, 54 against 64; MXFP4, whose tiles cost less to decode
+    // and gain from reuse, 165 against 140 and 53 against 62, but of one matrix 1000 x 2880 x 2816 28.6 against 30.2.
     const int cols = GLU ? 64 : 128;
-    if (a.offsets ? rows <= 16 : blocks(64, cols) < 128) launch_quant<OP, WTYPE, 1, 4, 1, 2, 3>(a, s);
-    else if (rows >= 256 && blocks(128, 2 * cols) >= 256) launch_quant<OP, WTYPE, 2, 4, 4, 4, 2>(a, s);
-    else launch_quant<OP, WTYPE, 2, 4, 2, 2, 2>(a, s);
+    if (rows >= 256 && blocks(128, 2 * cols) >= 256) launch_quant<OP, WTYPE, 2, 4, 4, 4, 2>(a, s);
+    else if (rows >= 256 && blocks(128, cols) >= 256) launch_quant<OP, WTYPE, 2, 4, 4, 2, 2>(a, s);
+    else if (!a.offsets && blocks(64, cols) < 128) launch_quant<OP, WTYPE, 1, 4, 1, 2, 3>(a, s);
+    else if (WTYPE == PE_W_INT4_G128 || !a.offsets || rows <= 16) launch_quant<OP, WTYPE, 1, 4, 2, 2, 2>(a, s);
+    else if constexpr (WTYPE != PE_W_INT4_G128) launch_quant<OP, WTYPE, 2, 4, 2, 2, 2>(a, s);
   } else {
     // 64 x 128 in four stages for few rows (8 experts of 64, GLU 768 x 2048: 19.7 against 26.3; 128 of 128: 284 against 227)
     if (rows <= 96) launch_rows<OP, true, 2, 4, 2, 2, 4>(a, s);

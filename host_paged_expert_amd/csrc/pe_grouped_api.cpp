@@ -249,7 +249,7 @@ int pe_combine_backward(int device, const void* dout, int64_t lddo, const int32_
   PE_TRY(check_dims(device, T, {k, H}));
   if (R < 0 || R >= kMaxRows) return fail(PE_ERR_INVALID_ARG, "R=%d outside [0, 2^24)", R);
   // a wavefront for each entry
-  if ((int64_t)T * k >= (1 << 26)) return fail(PE_ERR_INVALID_ARG, "T * top_k=%lld is not below 2^26", (long long)T * k);
+  if ((int64_t)T * k >= (1 << 25)) return fail(PE_ERR_INVALID_ARG, "T * top_k=%lld is not below 2^25", (long long)T * k);
   if (H % 8) return fail(PE_ERR_INVALID_ARG, "H must be a multiple of 8");
   if (T == 0) return PE_OK;
   if (!dy && !dtopk_w) return fail(PE_ERR_INVALID_ARG, "no gradient is asked for");

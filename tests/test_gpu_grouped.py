@@ -475,9 +475,10 @@ def _some(rng, n, count):
 
 WAYS_LINEAR = [(1, 2048, 1152), (8, 4096, 1152), (8, 4104, 1152), (16, 6144, 1152), (16, 2048, 1152), (17, 700, 1024),
                (144, 2048, 1152), (150, 2048, 1152), (200, 2048, 2176), (500, 2048, 256), (1000, 2048, 256),
-               (2048, 4096, 256), (2300, 4100, 384), (255, 33000, 128)]
+               (2048, 4096, 256), (2300, 4100, 384), (255, 33000, 128), (2048, 2048, 256), (2300, 2100, 384)]
 WAYS_GLU = [(4, 768, 1152), (9, 768, 1152), (16, 776, 1152), (8, 8192, 256), (8, 8208, 256), (144, 1024, 1152),
-            (200, 1024, 2176), (500, 1024, 256), (1000, 1024, 256), (2048, 2048, 256), (2300, 2056, 384)]
+            (200, 1024, 2176), (500, 1024, 256), (1000, 1024, 256), (2048, 2048, 256), (2300, 2056, 384), (2048, 1024, 256),
+            (2300, 1032, 384)]
 
 
 @pytest.mark.parametrize("T,N,K", WAYS_LINEAR)
@@ -513,7 +514,8 @@ def test_glu_w4_where_its_ways_change(T, I, H, wtype):
 # (experts, rows, columns, k): on average under 4 rows, up to 16, up to 96, more, 256 and more
 WAYS_GROUPED = [(3, 5, 64, 1152), (32, 97, 96, 1152), (40, 100, 2048, 1152), (30, 80, 8208, 256), (5, 12, 100, 256),
                 (4, 15, 200, 256), (4, 16, 200, 256), (4, 67, 200, 256), (4, 68, 200, 1152), (3, 290, 300, 256),
-                (3, 294, 300, 1152), (200, 2000, 136, 128), (2, 1100, 6704, 256), (130, 300, 72, 128), (1024, 900, 40, 128)]
+                (3, 294, 300, 1152), (200, 2000, 136, 128), (2, 1100, 6704, 256), (130, 300, 72, 128), (1024, 900, 40, 128),
+                (2, 1100, 3400, 256)]
 
 
 def _uneven(rng, E, R):

@@ -122,8 +122,10 @@ static void launch_group_rows_n(const GroupRowsArgs& a, hipStream_t s) {
 }
 
 void launch_group_rows(const GroupRowsArgs& a, hipStream_t s) {
-  if (a.n <= 1024) launch_group_rows_n<4, 4>(a, s);
-  else if (a.n <= 131072) launch_group_rows_n<16, 1>(a, s);
+  // Each workgroup reads all ids, so that the work grows as n squared once they no longer run all at once: entries of its
+  // own one a thread (128 experts, 32 ids 3.5 us against 7.1, 65536 10.3 against 18.4, 262144 29 against 36) up to a
+  // workgroup for each unit, eight beyond (1048576 ids 327 against 107).
+  if (a.n <= 262144) launch_group_rows_n<16, 1>(a, s);
   else launch_group_rows_n<16, 8>(a, s);
 }
 
@@ -169,9 +171,10 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
 }
 
 void launch_combine(const CombineArgs& a, hipStream_t s) {
+  // 8192 x 2 rows of 256: 4.0 us against 5.1; from 1024 columns on no slower so (8192 x 4 of 1024: 14.8 against 14.9,
+  // 8192 x 8 of 2048 48 against 64)
   const int chunks = a.H / 8;
   if (chunks <= 64) combine_kernel<64><<<dim3((a.T + 3) / 4, 1), 256, 0, s>>>(a);
-  else if (chunks <= 128) combine_kernel<128><<<dim3((a.T + 1) / 2, 1), 256, 0, s>>>(a);
   else combine_kernel<256><<<dim3(a.T, (chunks + 255) / 256), 256, 0, s>>>(a);
 }
 
@@ -265,7 +268,7 @@ __device__ __forceinline__ bool find_expert_tile(const GroupedArgs& a, int b, in
   int mine = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) mine += (max(o[i + 1] - o[i], 0) + BT - 1) / BT;
-  const int upto = prefix_sum(mine);
+  const int upto = prefix_sum(min(mine, 1 << 24));       // more than there can be: offsets that do not ascend
   const int row_tiles = __builtin_amdgcn_readlane(upto, 63);
   if (row_tiles > a.R / BT + min(a.E, a.R)) return false;        // offsets that do not ascend
   const int total = row_tiles * nn;

@@ -574,7 +574,7 @@ def test_grouped_ffn_backward_where_its_ways_change(E, R, H, I):
             _within(_np(got), ref, tol, "%s of expert %d" % (name, k))
 
 
-@pytest.mark.parametrize("T,k,E", [(128, 8, 70), (129, 8, 70), (16384, 8, 128), (16400, 8, 1024), (70000, 2, 3)])
+@pytest.mark.parametrize("T,k,E", [(128, 8, 70), (129, 8, 70), (16384, 8, 128), (16400, 8, 1024), (70000, 2, 3), (32768, 8, 128), (32800, 8, 1024)])
 def test_group_rows_of_many_entries(T, k, E):
     rng = np.random.default_rng(T + k)
     ids = np.minimum(rng.integers(-1, E, (T, k)), rng.integers(0, E + 1, (T, k))).astype(np.int32)

@@ -404,9 +404,10 @@ int pe_glu(int device, int wtype, int act, const void* x, int64_t ldx, const flo
  * gradients' error about 1.4 times that of one rounding.  w2 bf16 [hidden,
  * inter].  hidden and inter are multiples of 8.  x may be NULL without dw13,
  * w13 without dx.  A residual added to y has the gradient dy.  T = 0 sets dw13
- * and dw2 to zero.  This is the only gradient here: pe_forward, the norm, the
- * routing and pe_linear have none, so it serves the fitting of a shared expert
- * or dense block beside frozen experts, not the training of the whole layer. */
+ * and dw2 to zero.  Gradients are there for this, for experts that stay in GPU
+ * memory (pe_grouped_ffn_backward) and for the sum back to tokens
+ * (pe_combine_backward); pe_forward, the norm, the routing and pe_linear have
+ * none. */
 int pe_ffn_backward(int device, int act, const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* gu,
                     const void* w13, const void* w2, int T, int hidden, int inter, void* dgu, void* h, void* dx,
                     int64_t lddx, void* dw13, void* dw2, void* stream);

@@ -625,12 +625,11 @@ __global__ __launch_bounds__(WT * WN * 64) void grouped_weights_kernel(GroupedAr
 // The products sum_k x[k] w[k] take the codes' values as bf16, exactly, and a scale as far out as it is constant:
 //   MXFP4: an E2M1 value times its block's power of two is exact in bf16 (but for products beyond bf16's range, which
 //          are infinite, or below it), so v_cvt_scalef32_pk_bf16_fp4 makes operands that need nothing more.
-//   int4:  the fp16 scale of 128 k multiplies the fp32 sum over them.  The code q (0 .. 15) is an e4m3 number of value
-//          q 2^-9 (denormal below 8), so one v_cvt_scalef32_pk_bf16_fp8 makes two operands from bytes; and since
-//          sum x (q - 8) = sum x q - 8 sum x, the chain of MFMAs starts at -8 sum x, which an MFMA with a constant -8
-//          operand makes, once for all of a tile's weight rows.  Terms are so up to 15 |x| s where |q - 8| s |x| is
-//          meant: the fp32 error is that of sum |x| (q + 8) s.  (Subtracting 8 from the codes first takes twice
-//          the instructions.)
+//   int4:  the fp16 scale of 128 k multiplies the fp32 sum over them.  q ^ 8 as a signed 4-bit number is q - 8, and
+//          v_cvt_off_f32_i4 makes (q - 8) / 16 of it, of which the upper half is the bf16 number; the scale is taken
+//          times 16.  Every term is so x (q - 8) s and no other: a code of 8 adds nothing whatever x is, an infinity
+//          of x gives what its products with the weights give, and sums of 128 k pass fp32's range only where sum
+//          |x (q - 8)| / 16 does.
 
 namespace {
 
@@ -638,7 +637,7 @@ template <int WTYPE> constexpr bool kInt4 = WTYPE == PE_W_INT4_G128;
 template <int WTYPE> constexpr bool kMx = WTYPE == PE_W_MXFP4_B32;
 template <int WTYPE> constexpr int kScaleGroup = kInt4<WTYPE> ? 128 : 32;
 
-// Eight codes (the first in the lowest nibble) as bf16: int4 q, MXFP4 the value times `scale`.
+// Eight codes (the first in the lowest nibble) as bf16: int4 (q - 8) / 16, MXFP4 the value times `scale`.
 template <int WTYPE>
 __device__ __forceinline__ bf16x8_t decode8(uint32_t d, float scale) {
   typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
@@ -649,13 +648,17 @@ __device__ __forceinline__ bf16x8_t decode8(uint32_t d, float scale) {
     const bf16x2_t p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 3);
     return bf16x8_t{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
   } else {
-    const uint32_t even = d & 0x0F0F0F0Fu, odd = (d >> 4) & 0x0F0F0F0Fu;
-    const uint32_t lo = __builtin_amdgcn_perm(odd, even, 0x05010400u), hi = __builtin_amdgcn_perm(odd, even, 0x07030602u);
-    const bf16x2_t p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false);
-    const bf16x2_t p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true);
-    const bf16x2_t p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false);
-    const bf16x2_t p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true);
-    return bf16x8_t{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+    const uint32_t low = d ^ 0x88888888u;
+    uint32_t high = low >> 4;
+    asm("" : "+v"(high));                                // a shift for each code instead of each taking its byte, otherwise
+    uint32_t p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = __float_as_uint(__builtin_amdgcn_cvt_off_f32_i4((int)__builtin_amdgcn_ubfe(low, 8 * i, 8)));
+      const uint32_t b = __float_as_uint(__builtin_amdgcn_cvt_off_f32_i4((int)__builtin_amdgcn_ubfe(high, 8 * i, 8)));
+      p[i] = __builtin_amdgcn_perm(b, a, 0x07060302u);   // both numbers have zeros in their lower halves
+    }
+    return __builtin_bit_cast(bf16x8_t, make_uint4(p[0], p[1], p[2], p[3]));
   }
 }
 
@@ -664,12 +667,8 @@ __device__ __forceinline__ float e8m0(uint32_t e) {
   return __uint_as_float(e == 0 ? 0x00400000u : e == 255 ? 0x7FC00000u : e << 23);
 }
 
-__device__ __forceinline__ bf16x8_t minus8() {
-  const __bf16 v = (__bf16)-8.f;
-  return bf16x8_t{v, v, v, v, v, v, v, v};
-}
-
-__device__ __forceinline__ float half_value(uint16_t h) { return (float)__builtin_bit_cast(_Float16, h); }
+// What int4 sums are multiplied by: 16 times the fp16 scale.
+__device__ __forceinline__ float int4_scale(uint16_t h) { return 16.f * (float)__builtin_bit_cast(_Float16, h); }
 
 }  // namespace
 
@@ -776,15 +775,9 @@ __global__ __launch_bounds__(CW * KW * 64) void grouped_few_kernel(GroupedArgs g
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      f32x4_t start = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      if constexpr (kInt4<WTYPE>) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          start = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x[u][c]), minus8(), start, 0, 0, 0);
-      }
 #pragma unroll
       for (int f = 0; f < F; ++f) {
-        f32x4_t p = kInt4<WTYPE> ? start : acc[f];
+        f32x4_t p = kInt4<WTYPE> ? f32x4_t{0.f, 0.f, 0.f, 0.f} : acc[f];
         const float scale = kMx<WTYPE> ? e8m0(s[u][f]) : 0.f;
 #pragma unroll
         for (int c = 0; c < kX; ++c) {
@@ -798,7 +791,7 @@ __global__ __launch_bounds__(CW * KW * 64) void grouped_few_kernel(GroupedArgs g
           p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x[u][c]), v, p, 0, 0, 0);
         }
         if constexpr (kInt4<WTYPE>) {
-          const float by = half_value((uint16_t)s[u][f]);
+          const float by = int4_scale((uint16_t)s[u][f]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[f][i] = __builtin_fmaf(p[i], by, acc[f][i]);
         } else {
@@ -853,8 +846,8 @@ __global__ __launch_bounds__(CW * KW * 64) void grouped_few_kernel(GroupedArgs g
 // copied straight into LDS, the codes decoded by the wavefront that multiplies them.  A row's two 16-byte parts of a half
 // are exchanged in every other eight rows, so that the 16 rows of one read fall on all banks.  The scales of 1024 k lie
 // in LDS as well (as fp32, int4's by group, MXFP4's by row); those of the next 1024 wait in registers while these are
-// used.  2048 x 2048 x 6144: int4 81 us (0.63 PFLOP/s), MXFP4 61 (0.84); 4096 x 6144 x 6144 363 and 299 (0.85, 1.03): the
-// MFMAs that make -8 sum x are a quarter to a half of the others, and decoding costs as many cycles as they do.
+// used.  2048 x 2048 x 6144: int4 81 us (0.63 PFLOP/s), MXFP4 61 (0.84); 4096 x 6144 x 6144 363 and 299 (0.85, 1.03).
+// A wavefront decodes eight codes a lane in 69 clocks for int4 and 26 for MXFP4; the MFMA that takes them adds 10.
 template <DenseOp OP, int WTYPE, int WT, int WN, int FT, int FN, int NST>
 __global__ __launch_bounds__(WT * WN * 64) void quant_tile_kernel(GroupedArgs g) {
   constexpr int NW = WT * WN, BT = WT * FT * 16, BN = WN * FN * 16, kThreads = NW * 64;
@@ -952,7 +945,7 @@ __global__ __launch_bounds__(WT * WN * 64) void quant_tile_kernel(GroupedArgs g)
     for (int i = 0; i < kHeld; ++i) {
       const int idx = threadIdx.x + i * kThreads;
       if constexpr (kInt4<WTYPE>) {
-        *reinterpret_cast<float*>(scales + idx % 8 * kRow + idx / 8 * 4) = half_value((uint16_t)held[i]);
+        *reinterpret_cast<float*>(scales + idx % 8 * kRow + idx / 8 * 4) = int4_scale((uint16_t)held[i]);
       } else {
         f32x4_t v;
 #pragma unroll
@@ -994,14 +987,13 @@ __global__ __launch_bounds__(WT * WN * 64) void quant_tile_kernel(GroupedArgs g)
 #pragma unroll
       for (int s = 0; s < 4; ++s) af[s] = fa.bf16(st + (s >> 1) * kHalf, i, s & 1);
       if constexpr (kInt4<WTYPE>) {
-        f32x4_t start = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < 4; ++s) start = __builtin_amdgcn_mfma_f32_16x16x32_bf16(minus8(), af[s], start, 0, 0, 0);
         f32x4_t p[FN];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) p[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
-          for (int j = 0; j < FN; ++j) p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j][s], af[s], s ? p[j] : start, 0, 0, 0);
+          for (int j = 0; j < FN; ++j) p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j][s], af[s], p[j], 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll

@@ -430,9 +430,10 @@ int pe_ffn_backward(int device, int act, const void* dy, int64_t lddy, const voi
  *                   bytes from 253 on make them); byte 255 makes its 32
  *                   weights NaN.
  * Weights and scales are contiguous, those of E experts one after another.
- * x is bf16.  Sums are fp32.  int4 sums x (q - 8) as sum x q - 8 sum x, so their
- * error is that of terms |x| (q + 8) s; where x holds an infinity, or values
- * whose sum of 15 |x| passes fp32's range, the row's results are NaN or infinite.
+ * x is bf16.  Sums are fp32.  int4 sums x (q - 8) / 16, exact terms, over each 128
+ * k and takes the sums times 16 s: they pass fp32's range, and results are
+ * infinite or NaN, where 128 of |x (q - 8)| / 16 add up to it (|x| below 2^122
+ * never does).
  *
  * Rows grouped by expert: rows offsets[e] .. offsets[e+1] - 1 of a matrix of R
  * rows belong to expert e (offsets int32 [E + 1] on the device, ascending from 0

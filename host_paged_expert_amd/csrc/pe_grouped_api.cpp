@@ -251,7 +251,7 @@ int pe_combine_backward(int device, const void* dout, int64_t lddo, const int32_
   // a wavefront for each entry
   if ((int64_t)T * k >= (1 << 25)) return fail(PE_ERR_INVALID_ARG, "T * top_k=%lld is not below 2^25", (long long)T * k);
   if (H % 8) return fail(PE_ERR_INVALID_ARG, "H must be a multiple of 8");
-  if (T == 0) return PE_OK;
+  if (T == 0 || (R == 0 && !dtopk_w)) return PE_OK;   // (an empty dy has no address)
   if (!dy && !dtopk_w) return fail(PE_ERR_INVALID_ARG, "no gradient is asked for");
   const Mat mdo{"dout", dout, T, H, lddo, 2, 16}, mp{"places", places, 1, (int64_t)T * k, (int64_t)T * k, 4, 4};
   const Mat mw{"topk_w", topk_w, 1, (int64_t)T * k, (int64_t)T * k, 4, 4}, my{"y", y, R, H, ldy, 2, 16};

@@ -22,6 +22,15 @@ namespace pe {
 // theirs.  8192 x 8 ids, 128 experts: 11 us, where the bytes would take less than one: it is bound by the latency of its
 // passes, the counts' LDS atomics among them.  (A workgroup for each expert that numbers its entries took 24: entries of
 // one expert lie far apart, and each was a store of its own to lines that others write.)
+
+// The wavefront's lanes see each other's accesses to LDS in this order: LDS works a wavefront's off one after another,
+// the fences keep the compiler from moving one past here (a wave barrier by itself says nothing of memory).
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 template <int NW, int PER>
 __global__ __launch_bounds__(NW * 64) void group_rows_kernel(GroupRowsArgs a) {
   constexpr int kThreads = NW * 64, kOwn = kThreads * PER, kBatch = 8;
@@ -62,9 +71,9 @@ __global__ __launch_bounds__(NW * 64) void group_rows_kernel(GroupRowsArgs a) {
       const int rank = __popcll(same & ((1ull << lane) - 1));
       place[j] = counts[wave][id[j]] + rank;
     }
-    __builtin_amdgcn_wave_barrier();                     // all lanes have read before one of an expert's adds theirs
+    wave_order();                                        // all lanes have read before one of an expert's adds theirs
     if (in && (same & ((1ull << lane) - 1)) == 0) counts[wave][id[j]] += (uint16_t)__popcll(same);
-    __builtin_amdgcn_wave_barrier();
+    wave_order();
   }
   __syncthreads();
   // offsets: a prefix sum over the experts, E / (64 NW) of them a thread

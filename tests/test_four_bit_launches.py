@@ -32,3 +32,25 @@ def test_every_int4_kernel_is_run(shim):
     of_int4 = {k for k in kernels for op in (0, 1) for name in ("quant_tile", "grouped_few")
                if k.startswith("%s_kernel<%d,2," % (name, op))}
     assert len(of_int4) >= 15 and sorted(of_int4 - set(run)) == []
+
+
+def test_every_mxfp4_tile_is_run_with_k_that_ends_inside_a_step(shim):
+    calls = [("linear_w4",) + c + ("mxfp4",) for c in f.MX_LINEAR] + [("glu_w4",) + c + ("mxfp4",) for c in f.MX_GLU]
+    calls += _grouped_calls(f.MX_GROUPED, "mxfp4")
+    kernels, run = _launched(shim, calls)
+    tiles = {k for k in kernels for op in (0, 1) if k.startswith("quant_tile_kernel<%d,4," % op)}
+    assert len(tiles) == 10
+    for left in (32, 64, 96):
+        assert left in {c[-2] % 128 for c in calls}
+    for tile in tiles:
+        ks = {c[-2] for c, k in zip(calls, run) if k == tile}
+        assert ks and all(k % 128 for k in ks) and min(ks) < 192 and max(ks) > 1024, (tile, ks)
+
+
+def test_codes_and_scales_go_through_every_kernel(shim):
+    calls = [("linear_w4",) + c[1:] + c[:1] for c in f.PICKED_LINEAR] + [("glu_w4",) + c[1:] + c[:1] for c in f.PICKED_GLU]
+    for wtype in ("int4", "mxfp4"):
+        calls += _grouped_calls([c[1:] for c in f.PICKED_GROUPED if c[0] == wtype], wtype)
+    kernels, run = _launched(shim, calls)
+    assert sorted({k for k in kernels for w in (2, 4) for name in ("quant_tile", "grouped_few")
+                   for op in (0, 1) if k.startswith("%s_kernel<%d,%d," % (name, op, w))} - set(run)) == []

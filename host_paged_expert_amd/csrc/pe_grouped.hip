@@ -1076,13 +1076,25 @@ void launch_sized(const GroupedArgs& a, hipStream_t s) {
   constexpr bool GLU = OP == DENSE_GLU, Q = WTYPE != PE_W_BF16;
   const int rows = a.offsets ? a.R / std::min(a.E, a.R) : a.R;    // of a matrix, on average
   auto blocks = [&](int nr, int cols) { return row_tiles(a, nr) * ((a.d.N + cols - 1) / cols); };
-  // Streaming reads the weights once for every 16 rows, and is over when its workgroups are: grouped, 128 x 2 to 4 rows of
-  // GLU 768 x 2048 in int4 35 and 62, tiles 55 and 57; of one matrix, 96 x 2048 x 6144 25 against 34, 48 x 6144 x 2048 14.0
-  // and 14.0, GLU of 32 x 6144 x 2048 14.8 and 14.8 (576 and 768 workgroups), of 128 x 768 x 2048 10.4 against 14.0.
-  if (a.offsets ? rows < 4 && blocks(8, 8) < 1 << 24 : blocks(16, GLU ? 16 : 32) <= 576) {
+  // Streaming reads a matrix's weights once for every 16 rows and is over when its workgroups are; tiles read them once and
+  // keep more on the way, but are mostly empty where rows are few.  Streaming against tiles, by `few` workgroups:
+  // - one matrix: to 576 (int4 96 x 2048 x 6144 25 against 34, 48 x 6144 x 2048 14.0 and 14.0, GLU of 32 x 6144 x 2048
+  //   14.8 and 14.8, of 128 x 768 x 2048 10.4 against 14.0); of up to 4 rows and a longer k to 1024 (int4 1 x 32768 x
+  //   4096 22 against 28, 4 rows 24.5 against 28; 1 x 65536 x 2048 23.1 against 20.6, 1 x 32768 x 1024 10.9 against 10.2);
+  // - grouped, up to 16 rows a matrix on average, in 4 bits to 1024 of the workgroups that there can be (int4 GLU
+  //   768 x 2048, 4 experts of 4 rows 6.8 against 16, 8 of 16 12.2 against 16.7, 16 of 16 (1536) 16.1 against 16.8;
+  //   1536 x 2048, 24 of 4 (1200) 21.6 against 20.0), in bf16, with its bytes, to 288 (GLU 768 x 2048, 4 of 8 10.7
+  //   against 17.2, 4 of 24 (480) 18.3 against 16.3; 1536 x 2048, 12 of 4 (720) 19.2 against 16.8);
+  // - grouped, under 4 rows, whatever the workgroups: most experts that are reached have one or two (MXFP4 2880 x 2880,
+  //   24 of 2 34 against 47).  Where there are very many it is the slower (int4 GLU 768 x 2048, routed to 128 experts:
+  //   one row on average 36 against 33, two 50 against 45, three 62 against 49), as where one expert has most of the
+  //   rows (all 384 of one of 128: 34 against 17).
+  const int64_t few = blocks(16, GLU ? 16 : 32);
+  if (a.offsets ? (rows < 4 && blocks(8, 8) < 1 << 24) || (rows <= 16 && few <= (Q ? 1024 : 288))
+                : few <= (rows <= 4 && a.d.K > 1024 ? 1024 : 576)) {
     if constexpr (GLU) {
       // 16 rows, or 8 and two parts of k; where those are many, two workgroups' work in one (4 rows for 30 experts, int4
-      // 768 x 2048: 15.0 against 15.6; bf16 41.7 against 38.6).  (bf16 comes here grouped alone, with fewer rows.)
+      // 768 x 2048: 15.0 against 15.6; bf16 41.7 against 38.6).  (bf16 comes here grouped alone.)
       if constexpr (Q) {
         if (rows > 8) {
           launch_few<OP, WTYPE, 2, 1, 4, 1, 2>(a, s);

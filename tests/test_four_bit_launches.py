@@ -54,3 +54,20 @@ def test_codes_and_scales_go_through_every_kernel(shim):
     kernels, run = _launched(shim, calls)
     assert sorted({k for k in kernels for w in (2, 4) for name in ("quant_tile", "grouped_few")
                    for op in (0, 1) if k.startswith("%s_kernel<%d,%d," % (name, op, w))} - set(run)) == []
+
+
+def test_calls_of_few_rows_stream_their_weights(shim):
+    """A tile of 16 rows and more would be empty but for these: one matrix of many columns, and few experts of some rows
+    each.  Wider, or of more rows, they take tiles."""
+    streams, tiles = [], []
+    for w in ("int4", "mxfp4"):
+        streams += [("linear_w4", T, 32768, 4096, w) for T in (1, 4)] + [("glu_w4", T, 14336, 4096, w) for T in (1, 4)]
+        streams += [("glu", E, E * r, 768, 2048, w) for E, r in ((1, 16), (4, 4), (8, 8), (8, 16), (16, 4))]
+        streams += [("linear", E, E * r, 2048, 768, w) for E, r in ((2, 16), (4, 8), (8, 16))]
+        tiles += [("linear_w4", 1, 65536, 2048, w), ("linear_w4", 8, 32768, 4096, w), ("glu_w4", 1, 24576, 2048, w),
+                  ("linear_w4", 1, 32768, 1024, w), ("glu", 32, 32 * 4, 768, 2048, w), ("glu", 8, 8 * 17, 768, 2048, w)]
+    streams += [("glu", 4, 32, 768, 2048, "bf16"), ("glu", 2, 32, 768, 2048, "bf16"), ("linear", 4, 16, 1536, 2048, "bf16")]
+    tiles += [("glu", 4, 96, 768, 2048, "bf16"), ("linear", 12, 48, 1536, 2048, "bf16"), ("linear", 4, 68, 1536, 2048, "bf16")]
+    _, run = _launched(shim, streams + tiles)
+    for c, k in zip(streams + tiles, run):
+        assert k.startswith("grouped_few") == (c in streams), (c, k)

@@ -32,7 +32,7 @@ MX_LINEAR = [(150, 2048, 1056), (150, 2048, 96), (200, 2048, 2880), (500, 2048, 
              (2048, 2048, 288), (2048, 2048, 1056), (2300, 4100, 96), (2300, 4100, 1120)]
 MX_GLU = [(200, 1024, 2880), (150, 1088, 32), (500, 1024, 96), (500, 1024, 1056), (2048, 1024, 160), (2048, 1024, 1120),
           (2300, 2056, 1056), (2300, 2056, 64)]
-MX_GROUPED = [(4, 16, 200, 1120), (4, 16, 200, 32), (3, 14, 72, 2880), (3, 294, 300, 2880), (3, 294, 300, 96),
+MX_GROUPED = [(100, 700, 300, 1120), (100, 700, 300, 96), (4, 16, 200, 1120), (4, 16, 200, 32), (3, 14, 72, 2880), (3, 294, 300, 2880), (3, 294, 300, 96),
               (5, 300, 136, 1056), (2, 1100, 3400, 160), (2, 1100, 3400, 1056), (2, 1100, 6704, 96), (2, 1100, 6704, 1120)]
 
 

@@ -19,9 +19,11 @@ namespace pe {
 // A stable counting sort of the routed ids without scratch memory: every workgroup counts all ids by expert, those before
 // its own 64 NW PER apart, and so knows where its entries go without the others.  Among its own, a wavefront's come in
 // the order of its lanes (those of one expert find each other by a ballot for each bit of the id), wavefronts' in
-// theirs.  8192 x 8 ids, 128 experts: 11 us, where the bytes would take less than one: it is bound by the latency of its
-// passes, the counts' LDS atomics among them.  (A workgroup for each expert that numbers its entries took 24: entries of
-// one expert lie far apart, and each was a store of its own to lines that others write.)
+// theirs.  8192 x 8 ids of 128 experts: 10.4 us, where the bytes would take less than one.  It is bound by the counting:
+// equal ids among a wavefront's 64 add to one counter of LDS one after another, so that fewer experts take longer (8: 16.5,
+// 4: 23, 1: 58), and so does a list of one expert's ids (58).  Beyond a workgroup a unit it grows as n squared: 1048576
+// ids 111 us (of one expert 890), and 2^24, the most, 9.9 ms (113 ms).  (A workgroup for each expert that numbers its
+// entries took 24: entries of one expert lie far apart, and each was a store of its own to lines that others write.)
 
 // The wavefront's lanes see each other's accesses to LDS in this order: LDS works a wavefront's off one after another,
 // the fences keep the compiler from moving one past here (a wave barrier by itself says nothing of memory).
@@ -131,8 +133,8 @@ static void launch_group_rows_n(const GroupRowsArgs& a, hipStream_t s) {
 }
 
 void launch_group_rows(const GroupRowsArgs& a, hipStream_t s) {
-  // Each workgroup reads all ids, so that the work grows as n squared once they no longer run all at once: entries of its
-  // own one a thread (128 experts, 32 ids 3.5 us against 7.1, 65536 10.3 against 18.4, 262144 29 against 36) up to a
+  // Each workgroup reads all ids, so that the work grows as n squared once they no longer run all at once (here of 128
+  // experts): entries of its own one a thread (32 ids 3.5 us against 7.1, 65536 10.3 against 18.4, 262144 29 against 36) up to a
   // workgroup for each unit, eight beyond (1048576 ids 327 against 107).
   if (a.n <= 262144) launch_group_rows_n<16, 1>(a, s);
   else launch_group_rows_n<16, 8>(a, s);
@@ -143,7 +145,7 @@ void launch_group_rows(const GroupRowsArgs& a, hipStream_t s) {
 // out[t] = sum_j w[t, j] y[places[t, j]] + residual[t], in fp32 and in the order of
 // j: LPR lanes share a token's stretch of 8 LPR columns, each with 8 of them and
 // four rows of y in flight.  Bound by its bytes, each once: 8192 x 8 rows of 2048,
-// 336 MB, 68 us (4.9 TB/s, a large copy's rate).
+// 336 MB, 68 us (4.9 TB/s, a large copy's rate; 56 where the caches still hold some).
 template <int LPR>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
   const int64_t t = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
@@ -180,8 +182,8 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
 }
 
 void launch_combine(const CombineArgs& a, hipStream_t s) {
-  // 8192 x 2 rows of 256: 4.0 us against 5.1; from 1024 columns on no slower so (8192 x 4 of 1024: 14.8 against 14.9,
-  // 8192 x 8 of 2048 48 against 64)
+  // us of 64 lanes a row against 256, over four sets of rows in turn: 8192 x 2 rows of 256 5.2 against 7.1, 8192 x 8 of 512
+  // 15.5 against 18.5, 8192 x 4 of 1024 19.1 against 19.4, 8192 x 8 of 2048 88 against 68
   const int chunks = a.H / 8;
   if (chunks <= 64) combine_kernel<64><<<dim3((a.T + 3) / 4, 1), 256, 0, s>>>(a);
   else combine_kernel<256><<<dim3(a.T, (chunks + 255) / 256), 256, 0, s>>>(a);
@@ -507,9 +509,10 @@ __global__ __launch_bounds__(WT * WN * 64) void grouped_tile_kernel(GroupedArgs 
 // out[e][m, n] = sum over expert e's rows r of left[r, m] right[r, n]: both operands are k-slow, k being the expert's
 // rows, and an expert without rows gets zeros.  Rows of x come through the row list: its part for the next 32 steps lies
 // in LDS, where the copies of a step find their rows' addresses.  With some hundred rows to an expert its gradient is
-// hardly more than its bytes written: 128 experts of 128 rows, 1536 x 2048, 805 MB in 305 us.  Epilogues alone take 133
-// (6 TB/s), the sums 173, and what is left is the one waiting for the other's memory.  (Workgroups that went through all
-// tiles of some columns with copies running ahead, with or without wavefronts of their own for the stores: 420 to 540.)
+// hardly more than its bytes written: 128 experts of 128 rows, 1536 x 2048, 805 MB in 280 us, one call after another (305
+// to 310 behind the products of a backward pass).  Epilogues alone take 133 (6 TB/s), the sums 173: they hardly overlap.
+// (Workgroups that went through all tiles of some columns with copies running ahead, with or without wavefronts of their
+// own for the stores: 420 to 540.)
 template <bool GATHER, int WT, int WN, int FT, int FN, int NST>
 __global__ __launch_bounds__(WT * WN * 64) void grouped_weights_kernel(GroupedArgs g) {
   constexpr int NW = WT * WN, BT = WT * FT * 16, BN = WN * FN * 16, kList = 32;
@@ -606,7 +609,7 @@ __global__ __launch_bounds__(WT * WN * 64) void grouped_weights_kernel(GroupedAr
     }
   }
   // As finish_tile; the gradients are stored past the caches, which the rows of the tiles after them would lose otherwise
-  // (dw13 of 128 experts of 128 rows, 1536 x 2048: 373 us through them, 289 past them).
+  // (dw13 of 128 experts of 128 rows, 1536 x 2048: 340 us through them, 280 past them; dw2 169 and 155).
   constexpr int LR = BN + 4, kChunks = BN / 8;
   float* tile = reinterpret_cast<float*>(lds);
   wait_stage<0>();
@@ -689,8 +692,10 @@ __device__ __forceinline__ float int4_scale(uint16_t h) { return 16.f * (float)_
 // their sums, which meet in LDS in a fixed order.  A step is 128 bytes of k in bf16 and 64 bytes, 128 k, in 4 bits.  P
 // parts of k share the MFMA's 16 x 16 block as in the dense kernel of few rows.  x is the first operand, so that a lane's
 // accumulators belong to one weight row and its scale.
-// One row of int4 2048 x 6144, 6.4 MB: 5.1 us, of which a launch that does nothing is some 2.5.  Four rows to 30 of 128
-// experts, int4 GLU 768 x 2048, 45 MB: 15 us (3 TB/s), bf16 177 MB: 37 us (4.8 TB/s).
+// One row of int4 2048 x 6144, 6.4 MB: 5.3 us, of which a launch that does nothing is some 2.5.  Four rows to 30 of 128
+// experts, int4 GLU 768 x 2048, 45 MB: 16 us (2.8 TB/s), bf16 177 MB: 37 us (4.8 TB/s).  A workgroup waits for memory once
+// for its tile, and then for every KW P U steps: 4 rows of MXFP4 GLU 2880 x 2880 (23 steps, 16 a turn) take 7.4 us for
+// 8.9 MB.
 template <DenseOp OP, int WTYPE, int F, int CW, int KW, int P, int U>
 __global__ __launch_bounds__(CW * KW * 64) void grouped_few_kernel(GroupedArgs g) {
   static_assert(OP != DENSE_GLU || F == 2, "a gate and an up fragment");
@@ -855,7 +860,7 @@ __global__ __launch_bounds__(CW * KW * 64) void grouped_few_kernel(GroupedArgs g
 // copied straight into LDS, the codes decoded by the wavefront that multiplies them.  A row's two 16-byte parts of a half
 // are exchanged in every other eight rows, so that the 16 rows of one read fall on all banks.  The scales of 1024 k lie
 // in LDS as well (as fp32, int4's by group, MXFP4's by row); those of the next 1024 wait in registers while these are
-// used.  2048 x 2048 x 6144: int4 81 us (0.63 PFLOP/s), MXFP4 61 (0.84); 4096 x 6144 x 6144 363 and 299 (0.85, 1.03).
+// used.  2048 x 2048 x 6144: int4 76 us (0.68 PFLOP/s), MXFP4 62 (0.83); 4096 x 6144 x 6144 378 and 296 (0.82, 1.04).
 // A wavefront decodes eight codes a lane in 69 clocks for int4 and 26 for MXFP4; the MFMA that takes them adds 10.
 template <DenseOp OP, int WTYPE, int WT, int WN, int FT, int FN, int NST>
 __global__ __launch_bounds__(WT * WN * 64) void quant_tile_kernel(GroupedArgs g) {
@@ -1094,7 +1099,7 @@ void launch_sized(const GroupedArgs& a, hipStream_t s) {
                 : few <= (rows <= 4 && a.d.K > 1024 ? 1024 : 576)) {
     if constexpr (GLU) {
       // 16 rows, or 8 and two parts of k; where those are many, two workgroups' work in one (4 rows for 30 experts, int4
-      // 768 x 2048: 15.0 against 15.6; bf16 41.7 against 38.6).  (bf16 comes here grouped alone.)
+      // 768 x 2048: 17.6 against 19.2; bf16 41.7 against 38.6).  (bf16 comes here grouped alone.)
       if constexpr (Q) {
         if (rows > 8) {
           launch_few<OP, WTYPE, 2, 1, 4, 1, 2>(a, s);
@@ -1107,10 +1112,10 @@ void launch_sized(const GroupedArgs& a, hipStream_t s) {
       }
       launch_few<OP, WTYPE, 2, 1, 4, 2, 2>(a, s);
     } else {
-      // short sums: wavefronts for columns rather than for parts of k (30 experts, int4 2048 x 768: 10.0 against 11.5)
+      // short sums: wavefronts for columns rather than for parts of k (30 experts, int4 2048 x 768: 12.4 against 14.0)
       if (a.d.K <= 1024) launch_few<OP, WTYPE, 2, 2, 2, 1, 3>(a, s);
-      // the smallest workgroups while they are few (1 x 2048 x 6144: 4.4 against 5.4), 32 columns where those
-      // make 128 (16 x 6144 x 2048: 5.9 against 7.3), two parts of k otherwise (16 x 2048 x 6144: 7.4 against 11)
+      // the smallest workgroups while they are few (1 x 2048 x 6144: 5.5 against 6.7), 32 columns where those
+      // make 128 (16 x 6144 x 2048: 7.3 against 8.4), two parts of k otherwise (16 x 2048 x 6144: 9.0 against 15)
       else if (rows <= 8 && blocks(8, 8) <= 512) launch_few<OP, WTYPE, 1, 1, 4, 2, 2>(a, s);
       else if (blocks(16, 32) >= 128) launch_few<OP, WTYPE, 2, 1, 4, 1, 2>(a, s);
       else launch_few<OP, WTYPE, 2, 1, 4, 2, 2>(a, s);
@@ -1119,12 +1124,12 @@ void launch_sized(const GroupedArgs& a, hipStream_t s) {
   }
   if constexpr (Q) {
     // The largest tile that still fills the units where a matrix has the rows for it: 128 x 256 (4096 x 6144 x 6144, int4:
-    // 363 against 441 in 128 x 128 and 462 in 64 x 128), 128 x 128 (2048 x 2048 x 6144: 81 against 90 in 32 x 128
-    // and 88 in 64 x 128).
-    // Below, 16 x 128 where one matrix makes few workgroups (256 x 2048 x 2048: 13.5 against 15.3 in 32 x 128; 1000 x 2880
-    // x 2816: 48 against 34), and 32 x 128, of which more fit in a unit, against 64 x 128: int4, 32 experts of 128
-    // rows, 2880 x 2816, 127 against 144, 128 of 8, GLU 768 x 2048, 54 against 64; MXFP4, whose tiles cost less to decode
-    // and gain from reuse, 165 against 140 and 53 against 62, but of one matrix 1000 x 2880 x 2816 28.6 against 30.2.
+    // 378 against 438 in 128 x 128 and 493 in 64 x 128), 128 x 128 (2048 x 2048 x 6144: 76 against 96 in 32 x 128
+    // and 92 in 64 x 128).
+    // Below, 16 x 128 where one matrix makes few workgroups (256 x 2048 x 2048: 14.5 against 16.2 in 32 x 128; 1000 x 2880
+    // x 2816: 53 against 36), and 32 x 128, of which more fit in a unit, against 64 x 128: int4, 32 experts of 128
+    // rows, 2880 x 2816, 133 against 149, 128 of 8, GLU 768 x 2048, 53 against 66; MXFP4, whose tiles cost less to decode
+    // and gain from reuse, 167 against 136 and 54 against 62, but of one matrix 1000 x 2880 x 2816 29 against 30.
     const int cols = GLU ? 64 : 128;
     if (rows >= 256 && blocks(128, 2 * cols) >= 256) launch_quant<OP, WTYPE, 2, 4, 4, 4, 2>(a, s);
     else if (rows >= 256 && blocks(128, cols) >= 256) launch_quant<OP, WTYPE, 2, 4, 4, 2, 2>(a, s);

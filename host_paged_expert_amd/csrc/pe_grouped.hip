@@ -639,8 +639,8 @@ __global__ __launch_bounds__(WT * WN * 64) void grouped_weights_kernel(GroupedAr
 //          are infinite, or below it), so v_cvt_scalef32_pk_bf16_fp4 makes operands that need nothing more.
 //   int4:  the fp16 scale of 128 k multiplies the fp32 sum over them.  q ^ 8 as a signed 4-bit number is q - 8, and
 //          v_cvt_off_f32_i4 makes (q - 8) / 16 of it, of which the upper half is the bf16 number; the scale is taken
-//          times 16.  Every term is so x (q - 8) s and no other: a code of 8 adds nothing whatever x is, an infinity
-//          of x gives what its products with the weights give, and sums of 128 k pass fp32's range only where sum
+//          times 16.  Every term is so x (q - 8) s and no other: a code of 8 adds nothing to a finite x, an infinity of
+//          x gives what its products with the weights give, and sums of 128 k pass fp32's range only where sum
 //          |x (q - 8)| / 16 does.
 
 namespace {
@@ -662,7 +662,7 @@ __device__ __forceinline__ bf16x8_t decode8(uint32_t d, float scale) {
   } else {
     const uint32_t low = d ^ 0x88888888u;
     uint32_t high = low >> 4;
-    asm("" : "+v"(high));                                // a shift for each code instead of each taking its byte, otherwise
+    asm("" : "+v"(high));                                // one shift: the compiler would make one for each code
     uint32_t p[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

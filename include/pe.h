@@ -487,9 +487,9 @@ int pe_combine(int device, const void* y, int64_t ldy, int R, const int32_t* pla
 /* Gradients of pe_combine for dout bf16 [T, H]: dy[places[t,j]] = topk_w[t,j]
  * dout[t] (bf16 [R, H]; rows that no place names are left as they were) and
  * dtopk_w[t,j] = sum_h dout[t,h] y[places[t,j],h] (fp32 [T, top_k]; 0 for a place
- * outside [0, R)); either may be NULL, y may be without dtopk_w.  Two entries
- * must not have the same place if dy is asked for.  The residual's gradient is
- * dout.  T * top_k is below 2^25. */
+ * outside [0, R)); either may be NULL, y may be without dtopk_w.  With R = 0 and
+ * no dtopk_w there is nothing to do.  Two entries must not have the same place if
+ * dy is asked for.  The residual's gradient is dout.  T * top_k is below 2^25. */
 int pe_combine_backward(int device, const void* dout, int64_t lddo, const int32_t* places, const float* topk_w,
                         const void* y, int64_t ldy, int R, int T, int top_k, int H, void* dy, int64_t lddy,
                         float* dtopk_w, void* stream);
